@@ -19,11 +19,16 @@ from typing import Optional, Sequence, Tuple
 
 import numpy as np
 
+from . import kv4 as _kv4
+from .kv4 import (Kv4Cache, magi_bca_kv4_append, magi_bca_kv4_cache, magi_bca_kv4_evict, magi_bca_kv4_fwd,
+                  magi_bca_kv4_fwd_workspace_size, magi_bca_kv4_read, magi_bca_kv4_weights,
+                  magi_bca_kv4_weights_workspace_size)
+
 __all__ = ["magi_bca_fwd", "magi_bca_bwd", "magi_bca_fwd_rope", "magi_bca_bwd_rope", "magi_bca_bwd_noalloc",
            "magi_bca_bwd_workspace_size", "magi_bca_fwd_schedule", "magi_bca_release_caches", "magi_bca_cache_bytes",
            "magi_bca_status_string", "magi_bca_last_device_status", "magi_bca_profile_events", "MagiBcaError",
            "Dims", "library",
-           "library_path", "EXPORTED_SYMBOLS"]
+           "library_path", "EXPORTED_SYMBOLS"] + _kv4.__all__
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # MAGI_BCA_LIBRARY selects another build of the library (e.g. the bounds-checked
@@ -34,7 +39,9 @@ EXPORTED_SYMBOLS = ["magi_bca_fwd", "magi_bca_bwd", "magi_bca_bwd_workspace_size
                     "magi_bca_last_device_status", "magi_bca_fwd_schedule", "magi_bca_version",
                     "magi_bca_bwd_noalloc", "magi_bca_last_error_detail", "magi_bca_bwd_schedule",
                     "magi_bca_profile_events", "magi_bca_fwd_rope", "magi_bca_bwd_rope",
-                    "magi_bca_selftest_wait_timeout", "magi_bca_release_caches", "magi_bca_cache_bytes"]
+                    "magi_bca_selftest_wait_timeout", "magi_bca_release_caches", "magi_bca_cache_bytes",
+                    "magi_bca_kv4_append", "magi_bca_kv4_read", "magi_bca_kv4_fwd", "magi_bca_kv4_weights",
+                    "magi_bca_kv4_evict", "magi_bca_kv4_fwd_workspace_size", "magi_bca_kv4_weights_workspace_size"]
 
 
 class MagiBcaError(RuntimeError):
@@ -104,6 +111,7 @@ def library() -> ctypes.CDLL:
     lib.magi_bca_release_caches.restype = ctypes.c_int
     lib.magi_bca_cache_bytes.argtypes = []
     lib.magi_bca_cache_bytes.restype = ctypes.c_size_t
+    _kv4.declare(lib)
     _lib = lib
     return lib
 

@@ -17,8 +17,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmagi_bca.so")
 DEBUG_LIB = os.path.join(HERE, "libmagi_bca_debug.so")
-SOURCES = ["bca_api.cu", "bca_fwd.cu", "bca_bwd.cu", "bca_bwd_split.cu", "bca_noalloc.cu", "bca_sched.cpp"]
-DEPS = SOURCES + ["sm100.cuh", "bca_kernels.h", "bca_sched.h", "bca_norm.cuh", "bca_bwd_common.cuh", "bca_mask.cuh"]
+SOURCES = ["bca_api.cu", "bca_fwd.cu", "bca_bwd.cu", "bca_bwd_split.cu", "bca_noalloc.cu", "bca_sched.cpp",
+           "bca_kv4_api.cu", "bca_kv4_append.cu", "bca_kv4_token.cu", "bca_kv4_chunk.cu", "bca_kv4_evict.cu"]
+DEPS = SOURCES + ["sm100.cuh", "bca_kernels.h", "bca_sched.h", "bca_norm.cuh", "bca_bwd_common.cuh", "bca_mask.cuh",
+                  "bca_kv4.h", "bca_kv4.cuh", "bca_kv4_query.cuh"]
 
 
 def nvcc():
@@ -41,7 +43,7 @@ def build(force=False, verbose=False, debug=False):
     if not force and not needs_build(lib):
         return lib
     cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr",
+           "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr", "--threads", "8",
            "-I", os.path.join(ROOT, "include"), "-o", lib]
     if debug:
         cmd += ["-DMAGI_BCA_DEBUG"]

@@ -1,0 +1,110 @@
+// Internal interface of the 4-bit key/value cache: kernel parameters and
+// launchers, between bca_kv4_api.cu and the kernel files.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/magi_bca.h"
+
+namespace magi {
+namespace kv4 {
+
+// Device status codes of positions outside the cache (read as MAGI_BCA_DEVICE_CHECK).
+enum : int { kErrPosition = 3050 };
+
+// The cache with its strides; see magi_bca_kv4_cache.
+struct Cache {
+  uint8_t* kc;   // [B, H, cap, D/2]
+  uint8_t* ks;   // [B, H, cap, D/16]
+  uint8_t* vc;   // [B, H, cap/2, D]
+  uint8_t* vs;   // [B, H, cap/2, D/16, 2]
+  int batch, heads, dim, cap;
+};
+
+struct AppendParams {
+  Cache c;
+  const uint16_t* k;       // [B, n, H, D] bf16
+  const uint16_t* v;
+  const int32_t* start;    // [B]
+  const int32_t* counts;   // [B] or nullptr (n everywhere)
+  const float* rope;       // angles [(B,) n, D/2] or nullptr
+  int64_t rope_stride;     // elements from one batch element's angles to the next (0: shared)
+  int n;
+  float eps;
+  int heads_per_warp;
+  int* status;
+};
+
+struct ReadParams {
+  Cache c;
+  const int32_t* start;    // [B] or nullptr (0)
+  int n;
+  uint16_t* k;             // [B, n, H, D] bf16
+  uint16_t* v;
+};
+
+struct FwdParams4 {
+  Cache c;
+  const uint16_t* q;       // [B, Sq, Hq, D] bf16
+  const int32_t* lengths;  // [B]
+  const float* gamma_q;
+  const float* gamma_k;
+  const float* rope;       // angles [(B,) Sq, D/2] or nullptr
+  int64_t rope_stride;
+  const uint16_t* base_out;   // [B, Sq, Hq, D] bf16 or nullptr
+  const float* base_lse;      // [B, Hq, Sq]
+  uint16_t* out;
+  float* lse;                 // or nullptr
+  int heads_q, sq;
+  float scale_log2, eps;
+  int n_splits;            // parts of a history that different CTAs read
+  float* part_o;           // [n_splits, B, H, G * Sq, D] fp32
+  float2* part_ml;         // [n_splits, B, H, G * Sq] (reference in log2 units, sum)
+  uint16_t* qh;            // chunk path: folded queries [B, H, G * Sq, D] fp16 (high part)
+  uint16_t* ql;            //   and low part (weights only)
+  uint16_t* kx;            // chunk path: expanded keys [B, H, cap, D] fp16
+  uint16_t* vx;            //   and values
+  int rows_pad;            // weights, chunk path: G * Sq rounded up to 128
+  float* neg_lse;          //   -lse in log2 units [B, H, rows_pad], -inf behind the rows
+  const float* w_lse;      // weights: [B, Hq, Sq]
+  float* weights;          // weights: [B, H, cap]
+  float decay;
+  int* status;
+};
+
+struct EvictParams {
+  Cache src, dst;
+  const float* w_src;      // [B, H, src.cap]
+  float* w_dst;            // [B, H, dst.cap]
+  const int32_t* lengths;  // [B]
+  int32_t* new_lengths;    // [B]
+  int32_t* index;          // [B, H, keep]
+  int keep, recent;
+};
+
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_read(const ReadParams& p, cudaStream_t s);
+
+// Few query rows per key/value head: the rows of a head fit tiles of 8.
+constexpr int kTokenRows = 8;
+int token_splits(const Cache& c, int row_tiles);
+cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s);
+cudaError_t launch_token_weights(const FwdParams4& p, cudaStream_t s);
+cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s);
+
+// Many rows: expanded fp16 operands and the tensor cores of tcgen05.
+int chunk_splits(const Cache& c, int rows);
+int chunk_weight_splits(const Cache& c, int rows_pad);
+cudaError_t launch_expand(const FwdParams4& p, bool values, bool low, cudaStream_t s);
+cudaError_t launch_chunk_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
+                             cudaStream_t s);
+cudaError_t launch_chunk_weights(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk,
+                                 const FwdParams4& p, cudaStream_t s);
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
+
+}  // namespace kv4
+}  // namespace magi

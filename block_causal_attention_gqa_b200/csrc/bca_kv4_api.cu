@@ -1,0 +1,287 @@
+// C ABI of the 4-bit key/value cache: argument checks, the choice of kernels
+// and the workspace layout.  See include/magi_bca.h for the contract.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "bca_kernels.h"
+#include "bca_kv4.h"
+
+namespace magi {
+namespace kv4 {
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int check_cache(const magi_bca_kv4_cache* c) {
+  if (c == nullptr || c->k_codes == nullptr || c->k_scales == nullptr || c->v_codes == nullptr ||
+      c->v_scales == nullptr)
+    return MAGI_BCA_INVALID_ARG;
+  if (c->batch < 1 || c->heads_kv < 1 || c->capacity < 1) return MAGI_BCA_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return MAGI_BCA_UNSUPPORTED;
+  if (c->capacity % 128 != 0 || c->capacity > (1 << 30)) return MAGI_BCA_UNSUPPORTED;
+  if ((int64_t)c->batch * c->heads_kv > 65535) return MAGI_BCA_UNSUPPORTED;   // a grid dimension
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16))
+    return MAGI_BCA_INVALID_ARG;
+  return MAGI_BCA_OK;
+}
+
+Cache to_cache(const magi_bca_kv4_cache& c) {
+  return Cache{c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.batch, c.heads_kv, c.head_dim, c.capacity};
+}
+
+int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
+  if (q == nullptr || q->seqlen_q < 1 || q->heads_q < 1) return MAGI_BCA_INVALID_ARG;
+  if (!(q->rms_eps >= 0.f) || !(q->softmax_scale >= 0.f) || !std::isfinite(q->softmax_scale) ||
+      !std::isfinite(q->rms_eps) || q->rope_batch_stride < 0)
+    return MAGI_BCA_INVALID_ARG;
+  if (q->heads_q % c.heads_kv != 0) return MAGI_BCA_UNSUPPORTED;
+  if ((int64_t)c.batch * q->heads_q * q->seqlen_q >= (int64_t(1) << 31)) return MAGI_BCA_UNSUPPORTED;
+  return MAGI_BCA_OK;
+}
+
+int rows_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q) { return q.heads_q / c.heads_kv * q.seqlen_q; }
+
+// Which kernels: the token kernels read the cache once for each 8 rows (fwd)
+// or once in all (weights), the chunk kernels expand it to fp16 first.
+constexpr int kTokenFwdRows = 32;
+constexpr int kTokenWeightRows = 64;
+
+struct Plan {
+  bool token = true;
+  int splits = 1;
+  int rows_pad = 0;
+  size_t part_o = 0, part_ml = 0, qh = 0, ql = 0, kx = 0, vx = 0, neg_lse = 0, total = 0;
+};
+
+Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weights) {
+  Plan p;
+  const int rows = rows_of(c, q);
+  const Cache cc = to_cache(c);
+  const size_t BH = (size_t)c.batch * c.heads_kv, D = c.head_dim;
+  auto take = [&](size_t bytes) {
+    const size_t at = p.total;
+    p.total += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  p.token = rows <= (weights ? kTokenWeightRows : kTokenFwdRows);
+  p.rows_pad = (int)(((int64_t)rows + 127) / 128 * 128);
+  if (p.token) {
+    p.splits = token_splits(cc, weights ? 1 : (rows + kTokenRows - 1) / kTokenRows);
+  } else {
+    p.splits = weights ? chunk_weight_splits(cc, p.rows_pad) : chunk_splits(cc, rows);
+    p.qh = take(BH * rows * D * 2);
+    p.kx = take(BH * c.capacity * D * 2);
+    if (weights) {
+      p.ql = take(BH * rows * D * 2);
+      p.neg_lse = take(BH * p.rows_pad * 4);
+    } else {
+      p.vx = take(BH * c.capacity * D * 2);
+    }
+  }
+  if (p.splits > 1) {
+    if (!weights) {
+      p.part_o = take((size_t)p.splits * BH * rows * D * 4);
+      p.part_ml = take((size_t)p.splits * BH * rows * 8);
+    } else if (!p.token) {
+      p.part_o = take((size_t)p.splits * BH * c.capacity * 4);
+    }
+  }
+  return p;
+}
+
+FwdParams4 params_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, const Plan& plan, uint8_t* w) {
+  FwdParams4 p = {};
+  p.c = to_cache(c);
+  p.heads_q = q.heads_q;
+  p.sq = q.seqlen_q;
+  p.rope_stride = q.rope_batch_stride;
+  p.eps = q.rms_eps;
+  const float scale = q.softmax_scale > 0.f ? q.softmax_scale : 1.0f / std::sqrt((float)c.head_dim);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.n_splits = plan.splits;
+  p.rows_pad = plan.rows_pad;
+  p.part_o = reinterpret_cast<float*>(w + plan.part_o);
+  p.part_ml = reinterpret_cast<float2*>(w + plan.part_ml);
+  p.qh = reinterpret_cast<uint16_t*>(w + plan.qh);
+  p.ql = reinterpret_cast<uint16_t*>(w + plan.ql);
+  p.kx = reinterpret_cast<uint16_t*>(w + plan.kx);
+  p.vx = reinterpret_cast<uint16_t*>(w + plan.vx);
+  p.neg_lse = reinterpret_cast<float*>(w + plan.neg_lse);
+  return p;
+}
+
+int check_workspace(const Plan& plan, const void* workspace, size_t bytes) {
+  if (plan.total == 0) return MAGI_BCA_OK;
+  if (workspace == nullptr || !aligned(workspace, 256)) return MAGI_BCA_INVALID_ARG;
+  return bytes < plan.total ? MAGI_BCA_WORKSPACE_TOO_SMALL : MAGI_BCA_OK;
+}
+
+int done(const char* what, cudaError_t e) { return e == cudaSuccess ? MAGI_BCA_OK : record_cuda_failure(what, e); }
+
+}  // namespace
+}  // namespace kv4
+}  // namespace magi
+
+using namespace magi;
+using namespace magi::kv4;
+
+extern "C" {
+
+int magi_bca_kv4_append(const magi_bca_bf16* k, const magi_bca_bf16* v, const magi_bca_kv4_cache* cache,
+                        const int32_t* start, const int32_t* counts, int32_t n_tokens, const float* rope_k,
+                        int64_t rope_batch_stride, float rms_eps, void* stream) {
+  int st = check_cache(cache);
+  if (st != MAGI_BCA_OK) return st;
+  if (!k || !v || !start || n_tokens < 1 || rope_batch_stride < 0 || !(rms_eps >= 0.f) || !std::isfinite(rms_eps))
+    return MAGI_BCA_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16)) return MAGI_BCA_INVALID_ARG;
+  if (n_tokens > (1 << 30)) return MAGI_BCA_UNSUPPORTED;
+  AppendParams p = {};
+  st = device_status_word(&p.status);
+  if (st != MAGI_BCA_OK) return st;
+  p.c = to_cache(*cache);
+  p.k = k;
+  p.v = v;
+  p.start = start;
+  p.counts = counts;
+  p.n = n_tokens;
+  p.rope = rope_k;
+  p.rope_stride = rope_batch_stride;
+  p.eps = rms_eps;
+  return done("cache append launch", launch_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+int magi_bca_kv4_read(const magi_bca_kv4_cache* cache, const int32_t* start, int32_t n_tokens, magi_bca_bf16* k,
+                      magi_bca_bf16* v, void* stream) {
+  int st = check_cache(cache);
+  if (st != MAGI_BCA_OK) return st;
+  if (!k || !v || n_tokens < 1 || !aligned(k, 16) || !aligned(v, 16)) return MAGI_BCA_INVALID_ARG;
+  int* status;
+  st = device_status_word(&status);
+  if (st != MAGI_BCA_OK) return st;
+  return done("cache read launch",
+              launch_read(ReadParams{to_cache(*cache), start, n_tokens, k, v}, static_cast<cudaStream_t>(stream)));
+}
+
+size_t magi_bca_kv4_fwd_workspace_size(const magi_bca_kv4_cache* cache, const magi_bca_kv4_query* query) {
+  if (check_cache(cache) != MAGI_BCA_OK || check_query(*cache, query) != MAGI_BCA_OK) return 0;
+  return plan_of(*cache, *query, false).total;
+}
+
+size_t magi_bca_kv4_weights_workspace_size(const magi_bca_kv4_cache* cache, const magi_bca_kv4_query* query) {
+  if (check_cache(cache) != MAGI_BCA_OK || check_query(*cache, query) != MAGI_BCA_OK) return 0;
+  return plan_of(*cache, *query, true).total;
+}
+
+int magi_bca_kv4_fwd(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, const int32_t* lengths,
+                     const float* gamma_q, const float* gamma_k, const float* rope_q, const magi_bca_bf16* base_out,
+                     const float* base_lse, magi_bca_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                     const magi_bca_kv4_query* query, void* stream) {
+  int st = check_cache(cache);
+  if (st != MAGI_BCA_OK) return st;
+  st = check_query(*cache, query);
+  if (st != MAGI_BCA_OK) return st;
+  if (!q || !lengths || !gamma_q || !gamma_k || !out || (base_out == nullptr) != (base_lse == nullptr))
+    return MAGI_BCA_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(base_out, 16)) return MAGI_BCA_INVALID_ARG;
+  if (base_out == out || (lse != nullptr && base_lse == lse)) return MAGI_BCA_INVALID_ARG;
+  const Plan plan = plan_of(*cache, *query, false);
+  st = check_workspace(plan, workspace, workspace_bytes);
+  if (st != MAGI_BCA_OK) return st;
+  FwdParams4 p = params_of(*cache, *query, plan, static_cast<uint8_t*>(workspace));
+  st = device_status_word(&p.status);
+  if (st != MAGI_BCA_OK) return st;
+  p.q = q;
+  p.lengths = lengths;
+  p.gamma_q = gamma_q;
+  p.gamma_k = gamma_k;
+  p.rope = rope_q;
+  p.base_out = base_out;
+  p.base_lse = base_lse;
+  p.out = out;
+  p.lse = lse;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (plan.token) {
+    st = done("cache attention launch", launch_token_fwd(p, cs));
+  } else {
+    const int BH = cache->batch * cache->heads_kv, rows = rows_of(*cache, *query), D = cache->head_dim;
+    CUtensorMap tq, tk, tv;
+    if (make_tensor_map_bf16(&tq, p.qh, BH, rows, 1, D) != MAGI_BCA_OK ||
+        make_tensor_map_bf16(&tk, p.kx, BH, cache->capacity, 1, D) != MAGI_BCA_OK ||
+        make_tensor_map_bf16(&tv, p.vx, BH, cache->capacity, 1, D) != MAGI_BCA_OK)
+      return MAGI_BCA_CUDA_ERROR;
+    st = done("cache expansion launch", launch_expand(p, true, false, cs));
+    if (st == MAGI_BCA_OK) st = done("cache attention launch", launch_chunk_fwd(tq, tk, tv, p, cs));
+  }
+  if (st != MAGI_BCA_OK || plan.splits == 1) return st;
+  return done("cache attention combine launch", launch_combine(p, cs));
+}
+
+int magi_bca_kv4_weights(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, const int32_t* lengths,
+                         const float* lse, const float* gamma_q, const float* gamma_k, const float* rope_q,
+                         float* weights, float decay, void* workspace, size_t workspace_bytes,
+                         const magi_bca_kv4_query* query, void* stream) {
+  int st = check_cache(cache);
+  if (st != MAGI_BCA_OK) return st;
+  st = check_query(*cache, query);
+  if (st != MAGI_BCA_OK) return st;
+  if (!q || !lengths || !lse || !gamma_q || !gamma_k || !weights || !std::isfinite(decay)) return MAGI_BCA_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(weights, 16)) return MAGI_BCA_INVALID_ARG;
+  const Plan plan = plan_of(*cache, *query, true);
+  st = check_workspace(plan, workspace, workspace_bytes);
+  if (st != MAGI_BCA_OK) return st;
+  FwdParams4 p = params_of(*cache, *query, plan, static_cast<uint8_t*>(workspace));
+  st = device_status_word(&p.status);
+  if (st != MAGI_BCA_OK) return st;
+  p.q = q;
+  p.lengths = lengths;
+  p.gamma_q = gamma_q;
+  p.gamma_k = gamma_k;
+  p.rope = rope_q;
+  p.w_lse = lse;
+  p.weights = weights;
+  p.decay = decay;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (plan.token) return done("cache weights launch", launch_token_weights(p, cs));
+  const int BH = cache->batch * cache->heads_kv, rows = rows_of(*cache, *query), D = cache->head_dim;
+  CUtensorMap tqh, tql, tk;
+  if (make_tensor_map_bf16(&tqh, p.qh, BH, rows, 1, D) != MAGI_BCA_OK ||
+      make_tensor_map_bf16(&tql, p.ql, BH, rows, 1, D) != MAGI_BCA_OK ||
+      make_tensor_map_bf16(&tk, p.kx, BH, cache->capacity, 1, D) != MAGI_BCA_OK)
+    return MAGI_BCA_CUDA_ERROR;
+  st = done("cache expansion launch", launch_expand(p, false, true, cs));
+  if (st != MAGI_BCA_OK) return st;
+  return done("cache weights launch", launch_chunk_weights(tqh, tql, tk, p, cs));
+}
+
+int magi_bca_kv4_evict(const magi_bca_kv4_cache* cache, const float* weights, const int32_t* lengths, int32_t keep,
+                       int32_t recent, const magi_bca_kv4_cache* dst_cache, float* dst_weights, int32_t* dst_lengths,
+                       int32_t* index, void* stream) {
+  int st = check_cache(cache);
+  if (st != MAGI_BCA_OK) return st;
+  st = check_cache(dst_cache);
+  if (st != MAGI_BCA_OK) return st;
+  if (!weights || !lengths || !dst_weights || !dst_lengths || !index || keep < 1 || recent < 0 || recent > keep)
+    return MAGI_BCA_INVALID_ARG;
+  if (dst_cache->batch != cache->batch || dst_cache->heads_kv != cache->heads_kv ||
+      dst_cache->head_dim != cache->head_dim)
+    return MAGI_BCA_INVALID_ARG;
+  if (keep > dst_cache->capacity) return MAGI_BCA_INVALID_ARG;
+  // tokens move while others are still read: source and destination are different memory
+  if (dst_cache->k_codes == cache->k_codes || dst_cache->k_scales == cache->k_scales ||
+      dst_cache->v_codes == cache->v_codes || dst_cache->v_scales == cache->v_scales || dst_weights == weights ||
+      dst_lengths == lengths)
+    return MAGI_BCA_INVALID_ARG;
+  int* status;
+  st = device_status_word(&status);
+  if (st != MAGI_BCA_OK) return st;
+  return done("cache eviction launch",
+              launch_evict(EvictParams{to_cache(*cache), to_cache(*dst_cache), weights, dst_weights, lengths,
+                                       dst_lengths, index, keep, recent},
+                           static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

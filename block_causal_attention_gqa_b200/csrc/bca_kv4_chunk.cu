@@ -1,0 +1,694 @@
+// Attention of many query rows over the 4-bit cache, and the attention weight
+// its keys receive (whole chunks of the streaming layout).
+//
+// Mathematics as in bca_kv4_token.cu.  Here the tensor cores bound it: 4 D
+// flop per query, head and key for the attention, so a cached key is met by
+// thousands of rows and its conversion from 4 bits is best done once.
+// kv4_expand_kernel writes K^ and V as fp16 (exact: bca_kv4.cuh) and the folded
+// queries as fp16, and the two kernels below stream those through TMA into
+// tcgen05.  The expansion moves 5 bytes a value once; at 23040 keys of 8 heads
+// it is 1 % of the attention's time.  Converting inside the attention kernel
+// would repeat it for every 256 rows, on the issue slots of the softmax.
+//
+// Attention (kv4_chunk_fwd_kernel).  The rows of a key/value head (group heads
+// x queries, contiguous in the expanded queries) come in tiles of 128; a CTA
+// runs two of them against the same key/value tiles, with the roles and the
+// softmax of the forward kernel (bca_fwd.cu): warps 0-3 and 4-7 a softmax
+// warpgroup each, warp 8 issues the products, warp 9 the copies.  P is fp16 and
+// carries 2^7, the reference moves when a score passes it by 8.  A history is
+// cut into n_splits parts when the row tiles alone leave SMs idle.
+//
+// Weights (kv4_chunk_weights_kernel).  w_j sums over queries, so the tile is
+// turned: S^T = K^ Q^^T, a thread owns a key (a TMEM lane) and sums over the
+// queries in its registers, in a fixed order.  w_j is fp32, so the queries
+// enter as hi + lo (two products into one accumulator): 4 D flop per pair, on
+// the tensor cores while the CUDA cores take 2^(s - lse), one MUFU operation a
+// pair, 1024 clocks a tile for either.
+#include <algorithm>
+
+#include "bca_kv4.cuh"
+#include "bca_kv4_query.cuh"
+
+namespace magi {
+namespace kv4 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 320;
+constexpr int kStages = 2;
+constexpr float kMove = 8.f;
+constexpr float kLift = 7.f;
+
+enum : int {
+  kErrQ = 3111, kErrKFull, kErrVFull, kErrKEmpty, kErrVEmpty, kErrSFull, kErrPReady,
+  kErrWK = 3121, kErrWQFull, kErrWQEmpty, kErrWSFull, kErrWSEmpty, kErrWLse
+};
+
+// fp16 operands, fp32 accumulator (bits as make_idesc_bf16; A and B format 0 = fp16).
+__host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool ok, int* status, int code) {
+  if (ok) ok = mbar_wait(bar, parity, status, code);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// ------------------------------------------------------------------- expand
+//
+// Blocks [0, fold_blocks): folded queries, one warp a row (and, for the
+// weights, -lse in log2 units, padded with -inf to whole tiles).  The rest:
+// keys and values of the tokens below the length, rounded up to a tile of 128
+// (zeros there), in items of one key block (16 features of a token) or one
+// value block (8 features of two tokens).
+template <int D, bool kValues, bool kLow>
+__global__ void __launch_bounds__(256) kv4_expand_kernel(const FwdParams4 p, int fold_blocks) {
+  const int lane = threadIdx.x & 31;
+  const int G = p.heads_q / p.c.heads, rows = G * p.sq;
+  const int BH = p.c.batch * p.c.heads;
+  if ((int)blockIdx.x < fold_blocks) {
+    const int rows_pad = kLow ? p.rows_pad : rows;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < (int64_t)BH * rows_pad;
+         r += (int64_t)fold_blocks * 8) {
+      const int bh = (int)(r / rows_pad), row = (int)(r % rows_pad);
+      const int b = bh / p.c.heads, hk = bh % p.c.heads;
+      if (row < rows) {
+        uint32_t hi[D / 64], lo[D / 64];
+        fold_query<D>(p, b, hk, G, row, rows, lane, hi, lo);
+        const int64_t at = ((int64_t)bh * rows + row) * D + lane * (D / 32);
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint2*>(p.qh + at) = make_uint2(hi[0], hi[1]);
+          if (kLow) *reinterpret_cast<uint2*>(p.ql + at) = make_uint2(lo[0], lo[1]);
+        } else {
+          *reinterpret_cast<uint32_t*>(p.qh + at) = hi[0];
+          if (kLow) *reinterpret_cast<uint32_t*>(p.ql + at) = lo[0];
+        }
+      }
+      if (kLow && lane == 0) {
+        // rows behind the last, and rows that saw nothing, give no weight
+        const float x = row < rows ? p.w_lse[(int64_t)bh * rows + row] : -INFINITY;
+        p.neg_lse[(int64_t)bh * rows_pad + row] = x == -INFINITY ? -INFINITY : -x * kLog2e;
+      }
+    }
+    return;
+  }
+  constexpr int kPerTile = 128 * (D / 16);               // key blocks of a tile; as many value blocks
+  const int tiles = (p.c.cap + 127) / 128;
+  const int64_t items = (int64_t)BH * tiles;
+  for (int64_t it = (int64_t)blockIdx.x - fold_blocks; it < items; it += (int64_t)gridDim.x - fold_blocks) {
+    const int bh = (int)(it / tiles), tile = (int)(it % tiles);
+    const int len = min(max(__ldg(p.lengths + bh / p.c.heads), 0), p.c.cap);
+    if (tile * 128 >= len) continue;
+    const int64_t tok0 = (int64_t)bh * p.c.cap + tile * 128;
+    for (int i = threadIdx.x; i < kPerTile; i += 256) {
+      const int t = i / (D / 16), blk = i % (D / 16);
+      uint2 w = __ldg(reinterpret_cast<const uint2*>(p.c.kc + tok0 * (D / 2)) + i);
+      uint32_t s = scale_dup(__ldg(p.c.ks + tok0 * (D / 16) + i));
+      if (tile * 128 + t >= len) { w = make_uint2(0, 0); s = 0; }
+      uint32_t a[4], c[4];
+      codes_f16x8(w.x, a);
+      codes_f16x8(w.y, c);
+      uint4* dst = reinterpret_cast<uint4*>(p.kx + (tok0 + t) * D + blk * 16);
+      dst[0] = make_uint4(hmul2(a[0], s), hmul2(a[1], s), hmul2(a[2], s), hmul2(a[3], s));
+      dst[1] = make_uint4(hmul2(c[0], s), hmul2(c[1], s), hmul2(c[2], s), hmul2(c[3], s));
+    }
+    if constexpr (kValues) {
+      for (int i = threadIdx.x; i < 64 * (D / 8); i += 256) {
+        const int pr = i / (D / 8), f = i % (D / 8) * 8;   // row of two tokens, first of 8 features
+        const int64_t vrow = tok0 / 2 + pr;
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.c.vc + vrow * D + f));
+        const uint32_t s2 = __ldg(reinterpret_cast<const uint16_t*>(p.c.vs + (vrow * (D / 16) + f / 16) * 2));
+        uint32_t s = scale_pair(s2 & 0xffu, s2 >> 8);
+        const int t = tile * 128 + 2 * pr;
+        if (t + 1 >= len) s = t >= len ? 0u : s & 0xffffu;
+        uint32_t a[8];
+        codes_f16x8(w.x, reinterpret_cast<uint32_t(&)[4]>(a[0]));
+        codes_f16x8(w.y, reinterpret_cast<uint32_t(&)[4]>(a[4]));
+        uint32_t even[4], odd[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = hmul2(a[2 * k], s), y = hmul2(a[2 * k + 1], s);
+          even[k] = __byte_perm(x, y, 0x5410);
+          odd[k] = __byte_perm(x, y, 0x7632);
+        }
+        uint16_t* dst = p.vx + (tok0 + 2 * pr) * D + f;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(even[0], even[1], even[2], even[3]);
+        *reinterpret_cast<uint4*>(dst + D) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention
+template <int D>
+struct FwdLayout {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kBars = kV + kStages * kTile;
+  static constexpr int kTmemSlot = kBars + 16 * 8;
+  static constexpr int kAlloc = kTmemSlot + 16 + 1024;   // slack for 1024-byte alignment
+};
+
+struct FwdBars {
+  uint64_t q_full[2], s_full[2], p_ready[2];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+};
+
+template <int D>
+__device__ __forceinline__ void write_part(const FwdParams4& p, int split, int bh, int rows, int row, int f0, float m,
+                                           float l, const float (&o)[32]) {
+  const int64_t at = ((int64_t)split * p.c.batch * p.c.heads + bh) * rows + row;
+  if (f0 == 0) p.part_ml[at] = make_float2(m, l);
+  if (m == -INFINITY) return;
+#pragma unroll
+  for (int f = 0; f < 32; f += 4)
+    *reinterpret_cast<float4*>(p.part_o + at * D + f0 + f) = make_float4(o[f], o[f + 1], o[f + 2], o[f + 3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const FwdParams4 p) {
+  using L = FwdLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FwdBars* bars = reinterpret_cast<FwdBars*>(smem + L::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pairs = (int)gridDim.x / p.n_splits;
+  const int split = blockIdx.x / pairs, pair = blockIdx.x % pairs, bh = blockIdx.y;
+  const int b = bh / p.c.heads, hk = bh % p.c.heads;
+  const int G = p.heads_q / p.c.heads, rows = G * p.sq;
+  const int m0 = pair * 256;
+  const int n_sub = m0 + 128 < rows ? 2 : 1;
+  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  const int tiles = (len + 127) / 128;
+  const int t_begin = (int)((int64_t)tiles * split / p.n_splits);
+  const int n_vis = (int)((int64_t)tiles * (split + 1) / p.n_splits) - t_begin;
+  if (n_vis == 0) {   // nothing to see: the rows are the base part's, or empty
+    float zero[32] = {};
+    const int row = m0 + threadIdx.x;
+    if (threadIdx.x < 256 && row < rows) {
+      for (int f = 0; f < D; f += 32) {
+        if (p.n_splits > 1) write_part<D>(p, split, bh, rows, row, f, -INFINITY, 0.f, zero);
+        else finish_row<32>(p, b, hk, G, row, D, f, -INFINITY, 0.f, zero);
+      }
+    }
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_ready[s], 1);
+    }
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(&bars->k_full[st], 1);
+      mbar_init(&bars->k_empty[st], 1);
+      mbar_init(&bars->v_full[st], 1);
+      mbar_init(&bars->v_empty[st], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 9) {
+    if (elect_one()) {
+      for (int s = 0; s < n_sub; ++s) {
+        mbar_arrive_expect_tx(&bars->q_full[s], L::kTile);
+        for (int box = 0; box < D / 64; ++box)
+          tma_load_4d(smem + L::kQ + s * L::kTile + box * 16384, &tm_q, &bars->q_full[s], box * 64, 0, m0 + s * 128, bh);
+      }
+      for (int j = 0; j < n_vis; ++j) {
+        const int st = j % kStages;
+        const uint32_t par = ((j / kStages) & 1) ^ 1;
+        if (!mbar_wait(&bars->k_empty[st], par, p.status, kErrKEmpty)) break;
+        mbar_arrive_expect_tx(&bars->k_full[st], L::kTile);
+        for (int box = 0; box < D / 64; ++box)
+          tma_load_4d(smem + L::kK + st * L::kTile + box * 16384, &tm_k, &bars->k_full[st], box * 64, 0,
+                      (t_begin + j) * 128, bh);
+        if (!mbar_wait(&bars->v_empty[st], par, p.status, kErrVEmpty)) break;
+        mbar_arrive_expect_tx(&bars->v_full[st], L::kTile);
+        for (int box = 0; box < D / 64; ++box)
+          tma_load_4d(smem + L::kV + st * L::kTile + box * 16384, &tm_v, &bars->v_full[st], box * 64, 0,
+                      (t_begin + j) * 128, bh);
+      }
+    }
+  } else if (warp == 8) {
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = make_idesc_f16(128, 128, false);
+      constexpr uint32_t idesc_o = make_idesc_f16(128, D, true);
+      const uint32_t q_base = smem_u32(smem + L::kQ), k_base = smem_u32(smem + L::kK), v_base = smem_u32(smem + L::kV);
+      bool ok = true;
+      auto issue_s = [&](int s, int st) {
+        const uint32_t qa = q_base + s * L::kTile, ka = k_base + st * L::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_bf16_ss(tmem + 256 * s, make_sw128_desc(qa + off, 16, 1024), make_sw128_desc(ka + off, 16, 1024),
+                      idesc_s, kk > 0);
+        }
+      };
+      for (int s = 0; s < n_sub && ok; ++s) ok = mbar_wait(&bars->q_full[s], 0, p.status, kErrQ);
+      ok = ok && mbar_wait(&bars->k_full[0], 0, p.status, kErrKFull);
+      if (ok) {
+        tc_fence_after();
+        for (int s = 0; s < n_sub; ++s) {
+          issue_s(s, 0);
+          mma_commit(&bars->s_full[s]);
+        }
+        mma_commit(&bars->k_empty[0]);
+      }
+      for (int j = 0; j < n_vis && ok; ++j) {
+        const int st = j % kStages;
+        if (!mbar_wait(&bars->v_full[st], (j / kStages) & 1, p.status, kErrVFull)) break;
+        const bool has_next = j + 1 < n_vis;
+        const int st1 = (j + 1) % kStages;
+        for (int s = 0; s < n_sub; ++s) {
+          if (!mbar_wait(&bars->p_ready[s], j & 1, p.status, kErrPReady)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t va = v_base + st * L::kTile;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + 256 * s + 128, tmem + 256 * s + kk * 8, make_sw128_desc(va + kk * 2048, 16384, 1024),
+                        idesc_o, j > 0 || kk > 0);
+          if (has_next) {
+            if (s == 0 && !mbar_wait(&bars->k_full[st1], ((j + 1) / kStages) & 1, p.status, kErrKFull)) {
+              ok = false;
+              break;
+            }
+            issue_s(s, st1);
+          }
+          mma_commit(&bars->s_full[s]);
+        }
+        if (!ok) break;
+        mma_commit(&bars->v_empty[st]);
+        if (has_next) mma_commit(&bars->k_empty[st1]);
+      }
+    }
+  } else {
+    const int s = warp >> 2, r = threadIdx.x & 127;
+    if (s < n_sub) {
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lane_base + 256 * s;
+      const uint32_t t_o = tmem + lane_base + 256 * s + 128;
+      const int bar_id = 1 + s;
+      const int row = m0 + s * 128 + r;
+      bool ok = true;
+      float m_ref = -INFINITY, l_sum = 0.f;
+      for (int j = 0; j < n_vis; ++j) {
+        ok = warp_wait(&bars->s_full[s], j & 1, ok, p.status, kErrSFull);
+        if (ok) {
+          tc_fence_after();
+          uint64_t x2[64];
+          {
+            uint32_t raw[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, raw[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                x2[c * 16 + i] = f2_pack(__uint_as_float(raw[c][2 * i]), __uint_as_float(raw[c][2 * i + 1]));
+          }
+          const int lim = len - (t_begin + j) * 128;
+          const bool masked = lim < 128;   // the last tile only
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              float a0, a1;
+              f2_unpack(x2[c], a0, a1);
+              x2[c] = f2_pack(2 * c < lim ? a0 : -INFINITY, 2 * c + 1 < lim ? a1 : -INFINITY);
+            }
+          }
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a0, a1, b0, b1;
+            f2_unpack(x2[i], a0, a1);
+            f2_unpack(x2[4 + i], b0, b1);
+            mx[2 * i] = fmaxf(a0, b0);
+            mx[2 * i + 1] = fmaxf(a1, b1);
+          }
+#pragma unroll
+          for (int c = 8; c < 64; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float a0, a1, b0, b1;
+              f2_unpack(x2[c + i], a0, a1);
+              f2_unpack(x2[c + 4 + i], b0, b1);
+              mx[2 * i] = fmax3(mx[2 * i], a0, b0);
+              mx[2 * i + 1] = fmax3(mx[2 * i + 1], a1, b1);
+            }
+          const float m_tile = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          float alpha = 1.f;
+          if (m_tile > m_ref + kMove) {
+            alpha = fast_exp2(m_ref - m_tile);
+            m_ref = m_tile;
+            l_sum *= alpha;
+          }
+          const float nm = kLift - m_ref;   // every tile has a visible key, so m_ref is finite (or NaN)
+          const uint64_t shift = f2_pack(nm, nm);
+          uint64_t ls2[4] = {0, 0, 0, 0};
+          auto exp_row = [&](auto use_poly) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t a2 = f2_add(x2[c * 16 + i], shift);
+                float p0, p1;
+                if (decltype(use_poly)::value && (i & 3) == 3) {
+                  exp2_poly_pair(a2, p0, p1);
+                } else {
+                  float a0, a1;
+                  f2_unpack(a2, a0, a1);
+                  p0 = fast_exp2(a0);
+                  p1 = fast_exp2(a1);
+                }
+                ls2[i & 3] = f2_add(ls2[i & 3], f2_pack(p0, p1));
+                pk[i] = pack_f16x2(p0, p1);
+              }
+              tmem_st16(t_s + c * 16, pk);
+            }
+          };
+          if (masked)
+            exp_row(std::false_type{});
+          else
+            exp_row(std::true_type{});
+          {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(ls2[i], t[2 * i], t[2 * i + 1]);
+            l_sum += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+          }
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(t_o + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        named_bar_sync(bar_id, 128);
+        if (r == 0 && ok) mbar_arrive(&bars->p_ready[s]);
+      }
+      ok = warp_wait(&bars->s_full[s], n_vis & 1, ok, p.status, kErrSFull);
+      if (ok) {
+        tc_fence_after();
+        // scores that are NaN (a query that is) leave the reference at -inf: it
+        // must not pass for an empty row
+        const float m = m_ref == -INFINITY ? 0.f : m_ref - kLift;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t raw[32];
+          tmem_ld32(t_o + c * 32, raw);
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
+          if (row < rows) {
+            if (p.n_splits > 1) write_part<D>(p, split, bh, rows, row, c * 32, m, l_sum, o);
+            else finish_row<32>(p, b, hk, G, row, D, c * 32, m, l_sum, o);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ weights
+template <int D>
+struct WLayout {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kK = 0;
+  static constexpr int kQ = kTile;                         // stages of (hi, lo)
+  static constexpr int kLse = kQ + kStages * 2 * kTile;    // 4 x 128 floats
+  static constexpr int kSum = kLse + 4 * 512;              // 128 floats
+  static constexpr int kBars = kSum + 512;
+  static constexpr int kTmemSlot = kBars + 20 * 8;
+  static constexpr int kAlloc = kTmemSlot + 16 + 1024;
+};
+
+struct WBars {
+  uint64_t k_full, q_full[kStages], q_empty[kStages], s_full[4], s_empty[4], lse_full[4];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid_constant__ CUtensorMap tm_ql,
+                         const __grid_constant__ CUtensorMap tm_k, const FwdParams4 p) {
+  using L = WLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  WBars* bars = reinterpret_cast<WBars*>(smem + L::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = blockIdx.x, bh = blockIdx.y, split = blockIdx.z;
+  const int b = bh / p.c.heads;
+  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  if (tile * 128 >= len) return;
+  const int q_tiles = p.rows_pad / 128;
+  const int q_begin = (int)((int64_t)q_tiles * split / p.n_splits);
+  const int n = (int)((int64_t)q_tiles * (split + 1) / p.n_splits) - q_begin;   // >= 1: n_splits <= q_tiles
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->k_full, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_empty[i], 128);
+      mbar_init(&bars->lse_full[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&tm_qh);
+    tma_prefetch_desc(&tm_ql);
+    tma_prefetch_desc(&tm_k);
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 9) {
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&bars->k_full, L::kTile);
+      for (int box = 0; box < D / 64; ++box)
+        tma_load_4d(smem + L::kK + box * 16384, &tm_k, &bars->k_full, box * 64, 0, tile * 128, bh);
+      for (int j = 0; j < n; ++j) {
+        const int st = j % kStages, row = (q_begin + j) * 128;
+        if (!mbar_wait(&bars->q_empty[st], ((j / kStages) & 1) ^ 1, p.status, kErrWQEmpty)) break;
+        mbar_arrive_expect_tx(&bars->q_full[st], 2 * L::kTile);
+        uint8_t* dst = smem + L::kQ + st * 2 * L::kTile;
+        for (int box = 0; box < D / 64; ++box) {
+          tma_load_4d(dst + box * 16384, &tm_qh, &bars->q_full[st], box * 64, 0, row, bh);
+          tma_load_4d(dst + L::kTile + box * 16384, &tm_ql, &bars->q_full[st], box * 64, 0, row, bh);
+        }
+        const int sl = j & 3;
+        if (!mbar_wait(&bars->s_empty[sl], ((j >> 2) & 1) ^ 1, p.status, kErrWSEmpty)) break;
+        mbar_arrive_expect_tx(&bars->lse_full[sl], 512);
+        bulk_load(smem + L::kLse + sl * 512, p.neg_lse + (int64_t)bh * p.rows_pad + row, 512, &bars->lse_full[sl]);
+      }
+    }
+  } else if (warp == 8) {
+    if (elect_one()) {
+      constexpr uint32_t idesc = make_idesc_f16(128, 128, false);
+      const uint32_t k_base = smem_u32(smem + L::kK), q_base = smem_u32(smem + L::kQ);
+      bool ok = mbar_wait(&bars->k_full, 0, p.status, kErrWK);
+      for (int j = 0; j < n && ok; ++j) {
+        const int st = j % kStages, sl = j & 3;
+        ok = mbar_wait(&bars->q_full[st], (j / kStages) & 1, p.status, kErrWQFull) &&
+             mbar_wait(&bars->s_empty[sl], ((j >> 2) & 1) ^ 1, p.status, kErrWSEmpty);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            mma_bf16_ss(tmem + 128 * sl, make_sw128_desc(k_base + off, 16, 1024),
+                        make_sw128_desc(q_base + (st * 2 + part) * L::kTile + off, 16, 1024), idesc,
+                        part > 0 || kk > 0);
+          }
+        mma_commit(&bars->q_empty[st]);
+        mma_commit(&bars->s_full[sl]);
+      }
+    }
+  } else {
+    // warpgroup w takes the query tiles j = w, w + 2, ...; thread i owns key i of the tile
+    const int w = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    uint64_t s2[4] = {0, 0, 0, 0};
+    bool ok = true;
+    for (int j = w; j < n; j += 2) {
+      const int sl = j & 3;
+      ok = warp_wait(&bars->lse_full[sl], (j >> 2) & 1, ok, p.status, kErrWLse);
+      ok = warp_wait(&bars->s_full[sl], (j >> 2) & 1, ok, p.status, kErrWSFull);
+      if (!ok) break;
+      tc_fence_after();
+      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + L::kLse + sl * 512);
+      uint32_t raw[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + 128 * sl + c * 32, raw[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const ulonglong2 n2 = nl[c * 8 + i];   // -lse of four queries (the same for every key)
+          const uint64_t a = f2_add(f2_pack(__uint_as_float(raw[c][4 * i]), __uint_as_float(raw[c][4 * i + 1])), n2.x);
+          const uint64_t e = f2_add(f2_pack(__uint_as_float(raw[c][4 * i + 2]), __uint_as_float(raw[c][4 * i + 3])), n2.y);
+          float a0, a1, e0, e1;
+          f2_unpack(a, a0, a1);
+          f2_unpack(e, e0, e1);
+          s2[2 * (i & 1)] = f2_add(s2[2 * (i & 1)], f2_pack(fast_exp2(a0), fast_exp2(a1)));
+          s2[2 * (i & 1) + 1] = f2_add(s2[2 * (i & 1) + 1], f2_pack(fast_exp2(e0), fast_exp2(e1)));
+        }
+      tc_fence_before();
+      mbar_arrive(&bars->s_empty[sl]);
+    }
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(s2[i], t[2 * i], t[2 * i + 1]);
+    const float total = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+    float* sum = reinterpret_cast<float*>(smem + L::kSum);
+    if (w == 1) sum[r] = total;
+    named_bar_sync(1, 256);
+    if (w == 0 && ok && tile * 128 + r < len) {
+      const float x = total + sum[r];
+      const int64_t at = (int64_t)bh * p.c.cap + tile * 128 + r;
+      if (p.n_splits > 1) {
+        p.part_o[(int64_t)split * p.c.batch * p.c.heads * p.c.cap + at] = x;
+      } else {
+        p.weights[at] = p.decay != 0.f ? fmaf(p.decay, p.weights[at], x) : x;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the weights, in their order.
+__global__ void __launch_bounds__(256) kv4_weights_sum_kernel(const FwdParams4 p) {
+  const int bh = blockIdx.y, at = blockIdx.x * 256 + threadIdx.x;
+  const int len = min(max(__ldg(p.lengths + bh / p.c.heads), 0), p.c.cap);
+  if (at >= len) return;
+  const int64_t i = (int64_t)bh * p.c.cap + at, stride = (int64_t)p.c.batch * p.c.heads * p.c.cap;
+  float x = 0.f;
+  for (int s = 0; s < p.n_splits; ++s) x += p.part_o[s * stride + i];
+  p.weights[i] = p.decay != 0.f ? fmaf(p.decay, p.weights[i], x) : x;
+}
+
+template <int D>
+cudaError_t expand_d(const FwdParams4& p, bool values, bool low, cudaStream_t s) {
+  const int64_t rows = (int64_t)p.c.batch * p.c.heads * (low ? p.rows_pad : p.heads_q / p.c.heads * p.sq);
+  const int fold = (int)std::min<int64_t>((rows + 7) / 8, 148 * 16);
+  const int64_t tiles = (int64_t)p.c.batch * p.c.heads * ((p.c.cap + 127) / 128);
+  const int blocks = fold + (int)std::min<int64_t>(tiles, 148 * 16);
+  if (values) kv4_expand_kernel<D, true, false><<<blocks, 256, 0, s>>>(p, fold);
+  else kv4_expand_kernel<D, false, true><<<blocks, 256, 0, s>>>(p, fold);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t chunk_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
+                        cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv4_chunk_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdLayout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int rows = p.heads_q / p.c.heads * p.sq;
+  const dim3 grid((rows + 255) / 256 * p.n_splits, p.c.batch * p.c.heads);
+  kv4_chunk_fwd_kernel<D><<<grid, kThreads, FwdLayout<D>::kAlloc, s>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t chunk_weights_d(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk, const FwdParams4& p,
+                            cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kv4_chunk_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       WLayout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int BH = p.c.batch * p.c.heads;
+  kv4_chunk_weights_kernel<D><<<dim3(p.c.cap / 128, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s>>>(tqh, tql, tk, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.n_splits == 1) return e;
+  kv4_weights_sum_kernel<<<dim3((p.c.cap + 255) / 256, BH), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Parts of the history: a CTA takes 256 rows, one CTA runs on an SM.  Parts
+// are added while they fill more SMs, down to 4 tiles of a full cache each.
+int chunk_splits(const Cache& c, int rows) {
+  const int64_t units = (int64_t)c.batch * c.heads * ((rows + 255) / 256);
+  const int64_t want = std::max<int64_t>(1, 148 / units);
+  return (int)std::min<int64_t>({want, std::max<int64_t>(1, c.cap / 512), (int64_t)32});
+}
+
+// Parts of the queries, for the weights: a CTA takes a key tile.
+int chunk_weight_splits(const Cache& c, int rows_pad) {
+  const int64_t units = (int64_t)c.batch * c.heads * (c.cap / 128);
+  const int64_t want = std::max<int64_t>(1, 148 / units);
+  return (int)std::min<int64_t>({want, (int64_t)rows_pad / 128, (int64_t)32});
+}
+
+cudaError_t launch_expand(const FwdParams4& p, bool values, bool low, cudaStream_t s) {
+  return p.c.dim == 128 ? expand_d<128>(p, values, low, s) : expand_d<64>(p, values, low, s);
+}
+
+cudaError_t launch_chunk_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
+                             cudaStream_t s) {
+  return p.c.dim == 128 ? chunk_fwd_d<128>(tq, tk, tv, p, s) : chunk_fwd_d<64>(tq, tk, tv, p, s);
+}
+
+cudaError_t launch_chunk_weights(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk,
+                                 const FwdParams4& p, cudaStream_t s) {
+  return p.c.dim == 128 ? chunk_weights_d<128>(tqh, tql, tk, p, s) : chunk_weights_d<64>(tqh, tql, tk, p, s);
+}
+
+}  // namespace kv4
+}  // namespace magi

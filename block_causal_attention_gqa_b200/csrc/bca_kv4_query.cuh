@@ -1,0 +1,141 @@
+// The query side of the 4-bit cache's attention: the folded query
+//   Q^ = rot(q) r_q gamma_q gamma_k scale log2(e)
+// as two fp16 numbers, and the last step of a row.
+#pragma once
+#include "bca_kv4.cuh"
+
+namespace magi {
+namespace kv4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Row `row` of (b, hk)'s rows (group head g = row / Sq, query row % Sq), folded,
+// by one warp: lane holds features [lane*E, lane*E + E), E = D/32, as fp16
+// pairs hi and what they leave, lo.  A row behind the last is zero.
+template <int D>
+__device__ __forceinline__ void fold_query(const FwdParams4& p, int b, int hk, int G, int row, int rows, int lane,
+                                           uint32_t (&hi)[D / 64], uint32_t (&lo)[D / 64]) {
+  constexpr int E = D / 32;
+  float x[E] = {};
+  if (row < rows) {   // warp-uniform
+    const int h = hk * G + row / p.sq, i = row % p.sq;
+    const uint16_t* src = p.q + (((int64_t)b * p.sq + i) * p.heads_q + h) * D + lane * E;
+    if constexpr (E == 4) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+      x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+    } else {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src));
+      x[0] = bf16_lo(w); x[1] = bf16_hi(w);
+    }
+    const float r = rms_inv<D>(warp_sumsq_row<E>(x), p.eps);
+    if (p.rope != nullptr) {
+      float y[E];
+      rope_warp<D>(x, p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2), lane, y);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = y[e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = x[e] * r * qscale_of(p.gamma_q, p.gamma_k, p.scale_log2, lane * E + e);
+  }
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    hi[e / 2] = pack_f16x2(x[e], x[e + 1]);
+    const float2 back = __half22float2(*reinterpret_cast<__half2*>(&hi[e / 2]));
+    lo[e / 2] = pack_f16x2(x[e] - back.x, x[e + 1] - back.y);
+  }
+}
+
+// The same into shared memory in the order of mma.m16n8k16's A fragments with
+// hi in rows 0..7 and lo in rows 8..15: 16 bytes {hi, lo, hi, lo} per (k-step
+// j, lane (g, c)), where lane c's features of k-step j are c D/4 + 4j .. + 3.
+template <int D>
+__device__ __forceinline__ void fold_query_fragment(const FwdParams4& p, int b, int hk, int G, int row, int rows,
+                                                    int g, int lane, uint8_t* smem_q) {
+  uint32_t hi[D / 64], lo[D / 64];
+  fold_query<D>(p, b, hk, G, row, rows, lane, hi, lo);
+  const int d = lane * (D / 32), c = d / (D / 4), j = d % (D / 4) / 4;
+  uint8_t* dst = smem_q + (j * 32 + g * 4 + c) * 16;
+  if constexpr (D == 128)
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], lo[0], hi[1], lo[1]);
+  else
+    *reinterpret_cast<uint2*>(dst + (d % 4) / 2 * 8) = make_uint2(hi[0], lo[0]);
+}
+
+// N words (1, 2 or a multiple of 4), in pieces of up to 16 bytes.
+template <int N>
+__device__ __forceinline__ void load_words(const uint16_t* src, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i / 4);
+      w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+    w[0] = x.x; w[1] = x.y;
+  } else {
+    static_assert(N == 1, "1, 2 or a multiple of 4 words");
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_words(uint16_t* dst, const uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) reinterpret_cast<uint4*>(dst)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(dst) = w[0];
+  }
+}
+
+// The end of a row: O / l, joined with the base part if there is one, to bf16,
+// and the log of the sum.  The caller holds features [f0, f0 + F) of the row's
+// unnormalised O, with reference m (log2 units) and sum l; m = -inf: no key.
+template <int F>
+__device__ __forceinline__ void finish_row(const FwdParams4& p, int b, int hk, int G, int row, int D, int f0, float m,
+                                           float l, float (&o)[F]) {
+  const int h = hk * G + row / p.sq, i = row % p.sq;
+  const int64_t at = (((int64_t)b * p.sq + i) * p.heads_q + h) * D + f0;
+  const int64_t at_lse = ((int64_t)b * p.heads_q + h) * p.sq + i;
+  float lse = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+  float scale = m == -INFINITY ? 0.f : 1.f / l;
+  if (p.base_out != nullptr) {
+    const float base = __ldg(p.base_lse + at_lse);
+    const float top = fmaxf(lse, base);
+    if (!(lse == -INFINITY && base == -INFINITY)) {
+      const float a = expf(lse - top), e = expf(base - top);
+      const float both = a + e;
+      scale *= a / both;
+      const float share = e / both;
+      if (base != -INFINITY) {   // of an empty base part, base_out is not read
+        uint32_t w[F / 2];
+        load_words<F / 2>(p.base_out + at, w);
+#pragma unroll
+        for (int f = 0; f < F; f += 2) {
+          o[f] = fmaf(o[f], scale, bf16_lo(w[f / 2]) * share);
+          o[f + 1] = fmaf(o[f + 1], scale, bf16_hi(w[f / 2]) * share);
+        }
+        scale = 1.f;
+      }
+      lse = top + logf(both);
+    }
+  }
+  uint32_t w[F / 2];
+#pragma unroll
+  for (int f = 0; f < F; f += 2) w[f / 2] = sm100::pack_bf16x2(o[f] * scale, o[f + 1] * scale);
+  store_words<F / 2>(p.out + at, w);
+  if (p.lse != nullptr && f0 == 0) p.lse[at_lse] = lse;
+}
+
+}  // namespace kv4
+}  // namespace magi

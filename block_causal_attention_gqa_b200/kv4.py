@@ -1,0 +1,301 @@
+"""The key/value cache in 4 bits: binding of the ``magi_bca_kv4_*`` entry points.
+
+As the rest of the package this only marshals arguments; ``include/magi_bca.h``
+describes the format and each operation.  Lengths and positions are int32
+tensors on the device, so a decoding step can be captured in a CUDA graph and
+replayed while the history grows.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+__all__ = ["Kv4Cache", "magi_bca_kv4_cache", "magi_bca_kv4_append", "magi_bca_kv4_read", "magi_bca_kv4_fwd",
+           "magi_bca_kv4_weights", "magi_bca_kv4_evict", "magi_bca_kv4_fwd_workspace_size",
+           "magi_bca_kv4_weights_workspace_size"]
+
+
+class CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("batch", ctypes.c_int32), ("heads_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32)]
+
+
+class QueryStruct(ctypes.Structure):
+    _fields_ = [("seqlen_q", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("rms_eps", ctypes.c_float), ("rope_batch_stride", ctypes.c_int64)]
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    """Argument types of the entry points (called once, when the library is loaded)."""
+    vp, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    cp, qp = ctypes.POINTER(CacheStruct), ctypes.POINTER(QueryStruct)
+    lib.magi_bca_kv4_append.argtypes = [vp, vp, cp, vp, vp, i32, vp, i64, f32, vp]
+    lib.magi_bca_kv4_read.argtypes = [cp, vp, i32, vp, vp, vp]
+    lib.magi_bca_kv4_fwd.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, qp, vp]
+    lib.magi_bca_kv4_weights.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp, f32, vp, sz, qp, vp]
+    lib.magi_bca_kv4_evict.argtypes = [cp, vp, vp, i32, i32, cp, vp, vp, vp, vp]
+    for name in ("append", "read", "fwd", "weights", "evict"):
+        getattr(lib, "magi_bca_kv4_" + name).restype = ctypes.c_int
+    for name in ("fwd", "weights"):
+        f = getattr(lib, f"magi_bca_kv4_{name}_workspace_size")
+        f.argtypes, f.restype = [cp, qp], sz
+
+
+class Kv4Cache(NamedTuple):
+    """The four uint8 tensors of a cache (any 4-tuple of them will do):
+    k_codes [B, Hkv, capacity, D/2], k_scales [B, Hkv, capacity, D/16],
+    v_codes [B, Hkv, capacity/2, D], v_scales [B, Hkv, capacity/2, D/16, 2]."""
+    k_codes: "torch.Tensor"   # noqa: F821
+    k_scales: "torch.Tensor"  # noqa: F821
+    v_codes: "torch.Tensor"   # noqa: F821
+    v_scales: "torch.Tensor"  # noqa: F821
+
+
+def magi_bca_kv4_cache(batch: int, heads_kv: int, head_dim: int, capacity: int, device="cuda") -> Kv4Cache:
+    """A zeroed cache; capacity is rounded up to a multiple of 128 slots."""
+    import torch
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128 (got {head_dim})")
+    if min(batch, heads_kv, capacity) < 1:
+        raise ValueError("batch, heads_kv and capacity must be positive")
+    cap = -(-int(capacity) // 128) * 128
+    z = lambda *s: torch.zeros(*s, device=device, dtype=torch.uint8)  # noqa: E731
+    return Kv4Cache(z(batch, heads_kv, cap, head_dim // 2), z(batch, heads_kv, cap, head_dim // 16),
+                    z(batch, heads_kv, cap // 2, head_dim), z(batch, heads_kv, cap // 2, head_dim // 16, 2))
+
+
+def _struct(cache, device, name="cache") -> CacheStruct:
+    """Checks a cache's tensors and fills the C struct."""
+    import torch
+    kc, ks, vc, vs = cache
+    for part, t in (("k_codes", kc), ("k_scales", ks), ("v_codes", vc), ("v_scales", vs)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name}.{part} must be a contiguous uint8 CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name}.{part} is on {t.device}, the call runs on {device}")
+    if kc.dim() != 4:
+        raise ValueError(f"{name}.k_codes has shape {tuple(kc.shape)}, expected [batch, heads_kv, capacity, head_dim/2]")
+    B, H, cap, half = kc.shape
+    D = 2 * half
+    for part, t, shape in (("k_scales", ks, (B, H, cap, D // 16)), ("v_codes", vc, (B, H, cap // 2, D)),
+                           ("v_scales", vs, (B, H, cap // 2, D // 16, 2))):
+        if t.shape != shape:
+            raise ValueError(f"{name}.{part} has shape {tuple(t.shape)}, expected {shape}")
+    return CacheStruct(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), B, H, D, cap)
+
+
+def _check(name, t, dtype, shape, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    return t.data_ptr()
+
+
+def _check_rope(name, t, batch, n, half, device):
+    """(pointer, batch stride in elements) of an angle table [n, D/2] or [B, n, D/2]."""
+    import torch
+    if t is None:
+        return None, 0
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        return _check(name, t, torch.float32, (batch, n, half), device), n * half
+    return _check(name, t, torch.float32, (n, half), device), 0
+
+
+def _device_of(name, t, dims=4):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
+    return t.device
+
+
+def _call(name, device, stream, *args):
+    """Runs an entry point on `device`; the stream goes last."""
+    import torch
+    from . import MagiBcaError, _stream_handle, library
+    f = getattr(library(), name)
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, _stream_handle(stream, device))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _stream_handle(stream, device))
+    if st != 0:
+        raise MagiBcaError(st, name)
+
+
+def magi_bca_kv4_append(cache, k, v, start, counts=None, rope_k=None, rms_eps: float = 1e-6, stream=None) -> None:
+    """Quantises k, v [B, n, Hkv, D] bf16 into the slots start[b] .. of each
+    batch element (start: int32 [B] on the device).  counts: int32 [B], how many
+    of the n tokens are real (None: all).  rope_k: fp32 angles [n, D/2] or
+    [B, n, D/2] applied to k before its norm."""
+    import torch
+    dev = _device_of("k", k)
+    B, n, H, D = k.shape
+    c = _struct(cache, dev)
+    if (c.batch, c.heads_kv, c.head_dim) != (B, H, D):
+        raise ValueError(f"k has shape {tuple(k.shape)}, the cache holds batch {c.batch}, {c.heads_kv} heads of {c.head_dim}")
+    if n < 1:
+        return
+    kp = _check("k", k, torch.bfloat16, k.shape, dev)
+    vp = _check("v", v, torch.bfloat16, k.shape, dev)
+    sp = _check("start", start, torch.int32, (B,), dev)
+    np_ = _check("counts", counts, torch.int32, (B,), dev) if counts is not None else None
+    rp, rs = _check_rope("rope_k", rope_k, B, n, D // 2, dev)
+    _call("magi_bca_kv4_append", dev, stream, kp, vp, ctypes.byref(c), sp, np_, n, rp, rs, float(rms_eps))
+
+
+def magi_bca_kv4_read(cache, start, n: int, k=None, v=None, stream=None):
+    """The values of the slots start[b] .. start[b] + n - 1 (start None: from
+    slot 0) as bf16 (k, v) [B, n, Hkv, D]; the keys are normalised and rotated."""
+    import torch
+    dev = _device_of("cache.k_codes", cache[0])
+    c = _struct(cache, dev)
+    shape = (c.batch, int(n), c.heads_kv, c.head_dim)
+    k = torch.empty(shape, device=dev, dtype=torch.bfloat16) if k is None else k
+    v = torch.empty(shape, device=dev, dtype=torch.bfloat16) if v is None else v
+    kp = _check("k", k, torch.bfloat16, shape, dev)
+    vp = _check("v", v, torch.bfloat16, shape, dev)
+    sp = _check("start", start, torch.int32, (c.batch,), dev) if start is not None else None
+    if n > 0:
+        _call("magi_bca_kv4_read", dev, stream, ctypes.byref(c), sp, int(n), kp, vp)
+    return k, v
+
+
+def _query(q, c, gamma_q, gamma_k, rope_q, softmax_scale, rms_eps, dev):
+    """Checks the query side; returns (q, gamma_q, gamma_k, angles) pointers and the C struct."""
+    import torch
+    B, Sq, Hq, D = q.shape
+    if (c.batch, c.head_dim) != (B, D):
+        raise ValueError(f"q has shape {tuple(q.shape)}, the cache holds batch {c.batch}, heads of {c.head_dim}")
+    rp, rs = _check_rope("rope_q", rope_q, B, Sq, D // 2, dev)
+    ptrs = (_check("q", q, torch.bfloat16, q.shape, dev), _check("gamma_q", gamma_q, torch.float32, (D,), dev),
+            _check("gamma_k", gamma_k, torch.float32, (D,), dev), rp)
+    return ptrs, QueryStruct(Sq, Hq, float(softmax_scale), float(rms_eps), rs)
+
+
+def _workspace(size_fn, c, query, workspace, dev):
+    """(pointer, bytes, tensor) of the caller's workspace or a new one."""
+    import torch
+    from . import library
+    if workspace is None:
+        n = getattr(library(), size_fn)(ctypes.byref(c), ctypes.byref(query))
+        if n == 0:
+            return None, 0, None
+        workspace = torch.empty(n, device=dev, dtype=torch.uint8)
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the call runs on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _keep(tensor, stream):
+    """A workspace made here and used on a stream other than the current one
+    must not be handed out again before that stream is done with it."""
+    import torch
+    if tensor is not None and stream is not None and not torch.cuda.is_current_stream_capturing():
+        tensor.record_stream(stream)
+
+
+def magi_bca_kv4_fwd(q, cache, lengths, gamma_q, gamma_k, rope_q=None, base_out=None, base_lse=None, out=None,
+                     lse=None, softmax_scale: float = 0.0, rms_eps: float = 1e-6, want_lse: bool = True,
+                     workspace=None, stream=None):
+    """Attention of q [B, Sq, Hq, D] over the first lengths[b] (int32 [B] on the
+    device) tokens of the cache.  rope_q: angles [Sq, D/2] or [B, Sq, D/2].
+    base_out / base_lse: the same queries' attention over other keys, as
+    ``magi_bca_fwd`` returns it, to be joined.  Returns (out, lse)."""
+    import torch
+    dev = _device_of("q", q)
+    c = _struct(cache, dev)
+    (qp, gq, gk, rp), query = _query(q, c, gamma_q, gamma_k, rope_q, softmax_scale, rms_eps, dev)
+    B, Sq, Hq, D = q.shape
+    if (base_out is None) != (base_lse is None):
+        raise ValueError("base_out and base_lse go together")
+    if Sq < 1:
+        raise ValueError("q has no tokens")
+    out = torch.empty_like(q) if out is None else out
+    if lse is None and want_lse:
+        lse = torch.empty(B, Hq, Sq, device=dev, dtype=torch.float32)
+    op = _check("out", out, torch.bfloat16, q.shape, dev)
+    lp = _check("lse", lse, torch.float32, (B, Hq, Sq), dev) if lse is not None else None
+    bo = _check("base_out", base_out, torch.bfloat16, q.shape, dev) if base_out is not None else None
+    bl = _check("base_lse", base_lse, torch.float32, (B, Hq, Sq), dev) if base_lse is not None else None
+    ln = _check("lengths", lengths, torch.int32, (B,), dev)
+    wp, wb, ws = _workspace("magi_bca_kv4_fwd_workspace_size", c, query, workspace, dev)
+    _call("magi_bca_kv4_fwd", dev, stream, qp, ctypes.byref(c), ln, gq, gk, rp, bo, bl, op, lp, wp, wb,
+          ctypes.byref(query))
+    if workspace is None:
+        _keep(ws, stream)
+    return out, lse
+
+
+def magi_bca_kv4_weights(q, cache, lengths, lse, gamma_q, gamma_k, weights, rope_q=None, decay: float = 1.0,
+                         softmax_scale: float = 0.0, rms_eps: float = 1e-6, workspace=None, stream=None):
+    """weights[b, h, j] = decay * weights[b, h, j] + the attention weight key j
+    (j < lengths[b]) receives from q, given the rows' lse [B, Hq, Sq].  weights:
+    fp32 [B, Hkv, capacity], changed in place and returned."""
+    import torch
+    dev = _device_of("q", q)
+    c = _struct(cache, dev)
+    (qp, gq, gk, rp), query = _query(q, c, gamma_q, gamma_k, rope_q, softmax_scale, rms_eps, dev)
+    B, Sq, Hq, D = q.shape
+    if Sq < 1:
+        raise ValueError("q has no tokens")
+    lp = _check("lse", lse, torch.float32, (B, Hq, Sq), dev)
+    w = _check("weights", weights, torch.float32, (c.batch, c.heads_kv, c.capacity), dev)
+    ln = _check("lengths", lengths, torch.int32, (B,), dev)
+    wp, wb, ws = _workspace("magi_bca_kv4_weights_workspace_size", c, query, workspace, dev)
+    _call("magi_bca_kv4_weights", dev, stream, qp, ctypes.byref(c), ln, lp, gq, gk, rp, w, float(decay), wp, wb,
+          ctypes.byref(query))
+    if workspace is None:
+        _keep(ws, stream)
+    return weights
+
+
+def magi_bca_kv4_evict(cache, weights, lengths, keep: int, recent: int, dst_cache, dst_weights, dst_lengths=None,
+                       index=None, stream=None):
+    """Moves to dst_cache the last `recent` tokens of each (batch element, head)
+    and those with the largest weight, min(keep, length) in all, in their order;
+    dst_weights [B, Hkv, dst capacity] gets their weights.  Returns (dst_lengths
+    int32 [B], index int32 [B, Hkv, keep]: the slot each token came from, -1
+    behind the last)."""
+    import torch
+    dev = _device_of("cache.k_codes", cache[0])
+    c, d = _struct(cache, dev), _struct(dst_cache, dev, "dst_cache")
+    B, H = c.batch, c.heads_kv
+    if (d.batch, d.heads_kv, d.head_dim) != (B, H, c.head_dim):
+        raise ValueError("dst_cache must have the cache's batch, heads and head_dim")
+    keep, recent = int(keep), int(recent)
+    if not (1 <= keep <= d.capacity and 0 <= recent <= keep):
+        raise ValueError(f"need 1 <= keep <= {d.capacity} and 0 <= recent <= keep (got {keep}, {recent})")
+    w = _check("weights", weights, torch.float32, (B, H, c.capacity), dev)
+    dw = _check("dst_weights", dst_weights, torch.float32, (B, H, d.capacity), dev)
+    ln = _check("lengths", lengths, torch.int32, (B,), dev)
+    dst_lengths = torch.empty(B, device=dev, dtype=torch.int32) if dst_lengths is None else dst_lengths
+    index = torch.empty(B, H, keep, device=dev, dtype=torch.int32) if index is None else index
+    dl = _check("dst_lengths", dst_lengths, torch.int32, (B,), dev)
+    ix = _check("index", index, torch.int32, (B, H, keep), dev)
+    _call("magi_bca_kv4_evict", dev, stream, ctypes.byref(c), w, ln, keep, recent, ctypes.byref(d), dw, dl, ix)
+    return dst_lengths, index
+
+
+def _size(size_fn, cache, seqlen_q, heads_q):
+    from . import library
+    c = _struct(cache, cache[0].device)
+    return int(getattr(library(), size_fn)(ctypes.byref(c), ctypes.byref(QueryStruct(seqlen_q, heads_q, 0.0, 0.0, 0))))
+
+
+def magi_bca_kv4_fwd_workspace_size(cache, seqlen_q: int, heads_q: int) -> int:
+    """Bytes of workspace ``magi_bca_kv4_fwd`` needs for a cache of this shape."""
+    return _size("magi_bca_kv4_fwd_workspace_size", cache, seqlen_q, heads_q)
+
+
+def magi_bca_kv4_weights_workspace_size(cache, seqlen_q: int, heads_q: int) -> int:
+    """Bytes of workspace ``magi_bca_kv4_weights`` needs for a cache of this shape."""
+    return _size("magi_bca_kv4_weights_workspace_size", cache, seqlen_q, heads_q)

@@ -83,7 +83,8 @@ enum {
   MAGI_BCA_CUDA_ERROR = -5,         /* a CUDA runtime call failed (launch, copy, ...) */
   MAGI_BCA_DEVICE_TIMEOUT = -6,     /* a bounded device-side wait gave up */
   MAGI_BCA_DEVICE_CHECK = -7        /* a device-side bounds check failed (library built with
-                                     * -DMAGI_BCA_DEBUG: a work unit outside the problem) */
+                                     * -DMAGI_BCA_DEBUG: a work unit outside the problem; any build:
+                                     * magi_bca_kv4_append to a slot outside the cache) */
 };
 
 typedef struct {
@@ -297,6 +298,120 @@ int64_t magi_bca_fwd_schedule(const int32_t* q_chunk_offsets, const int32_t* kv_
  * units (writing at most `capacity`), or a negative status. */
 int64_t magi_bca_bwd_schedule(const int32_t* q_chunk_offsets, const int32_t* kv_chunk_offsets,
                               const magi_bca_dims* dims, int32_t num_sms, int32_t* units, int64_t capacity);
+
+/* ------------------------------------------------------------------------
+ * The key/value cache in 4 bits, for streaming inference (MAGI-1 §2.4.4: a KV
+ * cache of clean chunks): append finished keys and values, attend to them,
+ * accumulate the attention weight each key receives, and keep the keys with
+ * most of it.  The cache holds the history; the active chunks attend among
+ * themselves through magi_bca_fwd, whose (out, lse) magi_bca_kv4_fwd joins.
+ *
+ * A value is c * s: c in 4 bits (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6), s the scale of 16 neighbouring features in 8 bits (5
+ * exponent bits, 3 mantissa bits, no sign; byte << 7 is the scale in fp16; at
+ * most 10240).  s = max|x| / 6 and c = x / s, both to nearest, ties to even.
+ * Every cached value is exact in bf16 and fp16.  Magnitudes over 61440 are
+ * stored as 61440, values of a block whose maximum is below 6 * 2^-18 as zero,
+ * NaN as zero.
+ *
+ * Keys are stored as the attention reads them, rot(k) / RMS(k), so that a
+ * history needs neither angles nor norms; gamma_k is applied to the query.  A
+ * key row with a value that is not finite is stored as zeros.  Values are
+ * stored as they are.
+ *
+ * Tokens of a batch element fill the slots [0, length); the lengths live in
+ * device memory, so that a captured graph replays with growing histories.
+ * Slots from `length` on may hold anything and are neither read for a result
+ * nor written by any call but append.  No call allocates, synchronises or
+ * copies; all can be captured in a CUDA graph.  Calls that use the same cache
+ * or workspace must be ordered (one stream, or events). */
+typedef struct {
+  uint8_t* k_codes;  /* [batch, heads_kv, capacity, head_dim / 2]: byte i holds feature 2i in its low half
+                      * and 2i + 1 in its high half */
+  uint8_t* k_scales; /* [batch, heads_kv, capacity, head_dim / 16] */
+  uint8_t* v_codes;  /* [batch, heads_kv, capacity / 2, head_dim]: byte d of row p holds feature d of token
+                      * 2p in its low half and of token 2p + 1 in its high half */
+  uint8_t* v_scales; /* [batch, heads_kv, capacity / 2, head_dim / 16, 2]: last axis token 2p, 2p + 1 */
+  int32_t batch;
+  int32_t heads_kv;  /* batch * heads_kv <= 65535 */
+  int32_t head_dim;  /* 64 or 128 */
+  int32_t capacity;  /* slots of each (batch element, head); a multiple of 128 */
+} magi_bca_kv4_cache; /* device pointers, 16-byte aligned, caller-owned */
+
+typedef struct {
+  int32_t seqlen_q;
+  int32_t heads_q;            /* heads_q % heads_kv == 0 */
+  float softmax_scale;        /* 0 selects 1/sqrt(head_dim) */
+  float rms_eps;              /* >= 0 */
+  int64_t rope_batch_stride;  /* elements from one batch element's angles to the next; 0 = shared */
+} magi_bca_kv4_query;
+
+/* Quantises k, v [batch, n_tokens, heads_kv, head_dim] bf16 into the slots
+ * [start[b], start[b] + counts[b]) of each batch element b.  start and counts
+ * are device int32 [batch]; counts (NULL: n_tokens everywhere) is how many of
+ * the tokens are real, the rest is padding and not written.  rope_k [n_tokens,
+ * head_dim/2] (or one such table for each batch element, rope_batch_stride
+ * apart) are the tokens' angles, or NULL.  Overwriting slots is allowed.  A
+ * token whose slot is outside the cache is not written and sets
+ * MAGI_BCA_DEVICE_CHECK in the device status word. */
+int magi_bca_kv4_append(const magi_bca_bf16* k, const magi_bca_bf16* v, const magi_bca_kv4_cache* cache,
+                        const int32_t* start, const int32_t* counts, int32_t n_tokens, const float* rope_k,
+                        int64_t rope_batch_stride, float rms_eps, void* stream);
+
+/* The values of the slots [start[b], start[b] + n_tokens) as bf16 [batch,
+ * n_tokens, heads_kv, head_dim] (start NULL: from slot 0).  A slot outside the
+ * cache reads as zeros.  The keys are normalised and rotated ones. */
+int magi_bca_kv4_read(const magi_bca_kv4_cache* cache, const int32_t* start, int32_t n_tokens, magi_bca_bf16* k,
+                      magi_bca_bf16* v, void* stream);
+
+/* Bytes of device workspace the two calls below need (256-byte aligned; may be
+ * 0, then NULL is fine); 0 if an argument is invalid.  Depends on the cache's
+ * shape, not on the lengths.  Contents on entry do not matter. */
+size_t magi_bca_kv4_fwd_workspace_size(const magi_bca_kv4_cache* cache, const magi_bca_kv4_query* query);
+size_t magi_bca_kv4_weights_workspace_size(const magi_bca_kv4_cache* cache, const magi_bca_kv4_query* query);
+
+/* Attention of q [batch, seqlen_q, heads_q, head_dim] over the first
+ * lengths[b] (device int32 [batch]; clamped to [0, capacity]) tokens of the
+ * cache; every query sees all of them.  rope_q: the queries' angles
+ * [seqlen_q, head_dim/2] (see rope_batch_stride) or NULL.
+ *   base_out, base_lse (both or neither): the attention of the same queries
+ * over other keys, as magi_bca_fwd gives it (out and natural-log lse); the
+ * result is the attention over both sets of keys together.  A base_lse of -inf
+ * marks a row with no other keys; base_out of it is not read.  They must not
+ * overlap out and lse.
+ *   out bf16, lse fp32 [batch, heads_q, seqlen_q] (NULL: not wanted).  A row
+ * with no key at all gets out = 0 and lse = -inf.
+ * Repeated calls give the same bits. */
+int magi_bca_kv4_fwd(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, const int32_t* lengths,
+                     const float* gamma_q, const float* gamma_k, const float* rope_q, const magi_bca_bf16* base_out,
+                     const float* base_lse, magi_bca_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                     const magi_bca_kv4_query* query, void* stream);
+
+/* The attention weight the cached keys receive from q: for j < lengths[b],
+ *   weights[b, h, j] = decay * weights[b, h, j] + sum over the group's heads
+ *                      and the queries i of exp(s_ij - lse_i),
+ * with lse [batch, heads_q, seqlen_q] the log of the whole softmax sum (the lse
+ * of magi_bca_kv4_fwd, own block included).  weights: fp32 [batch, heads_kv,
+ * capacity], 16-byte aligned; entries from lengths[b] on stay as they are.
+ * decay 1 accumulates, 0 replaces (old contents are not read).  A row whose lse
+ * is -inf gives no weight.  Repeated calls give the same bits. */
+int magi_bca_kv4_weights(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, const int32_t* lengths,
+                         const float* lse, const float* gamma_q, const float* gamma_k, const float* rope_q,
+                         float* weights, float decay, void* workspace, size_t workspace_bytes,
+                         const magi_bca_kv4_query* query, void* stream);
+
+/* Keeps min(keep, lengths[b]) tokens of each (batch element, head) and moves
+ * them, in order, to slots [0, that) of dst_cache: the last `recent` ones
+ * (recent <= keep) and, of the others, those with the largest weight (equal
+ * weights: the lower slot; NaN counts as -inf).  Their weights move to
+ * dst_weights [batch, heads_kv, dst capacity], the new lengths to dst_lengths
+ * [batch], and index [batch, heads_kv, keep] (int32) gets the slot each came
+ * from, -1 behind the last.  keep <= dst capacity.  dst_cache, dst_weights and
+ * dst_lengths must not overlap the source; the source is not changed, nor are
+ * dst slots behind the new length. */
+int magi_bca_kv4_evict(const magi_bca_kv4_cache* cache, const float* weights, const int32_t* lengths, int32_t keep,
+                       int32_t recent, const magi_bca_kv4_cache* dst_cache, float* dst_weights, int32_t* dst_lengths,
+                       int32_t* index, void* stream);
 
 /* Library version string. */
 const char* magi_bca_version(void);

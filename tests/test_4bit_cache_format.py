@@ -1,0 +1,189 @@
+"""The 4-bit key/value cache without a GPU: the reference's format pinned by
+hand, and every refusal of the C entry points and the binding that comes
+before device work."""
+import ctypes
+
+import pytest
+import torch
+
+import block_causal_attention_gqa_b200 as bca
+from block_causal_attention_gqa_b200.kv4 import CacheStruct, QueryStruct
+from tests import kv4_reference as ref
+
+OK, INVALID, UNSUPPORTED, TOO_SMALL = 0, -1, -2, -4
+
+
+# ------------------------------------------------------------ the format itself
+def test_scale_bytes_are_fp16_numbers():
+    """byte << 7 read as fp16 is the table's value, subnormals included."""
+    bits = (torch.arange(248, dtype=torch.int32) << 7).to(torch.int16)
+    assert torch.equal(bits.view(torch.float16).double(), ref.SCALES[:248])
+    assert ref.SCALES[ref.TOP_BYTE] == 10240
+
+
+def test_every_cached_value_is_exact_in_bf16_and_fp16():
+    vals = ref.SCALES[: ref.TOP_BYTE + 1, None] * ref.MAGS
+    assert torch.equal(vals.to(torch.bfloat16).double(), vals)
+    assert torch.equal(vals.to(torch.float16).double(), vals)
+
+
+@pytest.mark.parametrize("x,code", [(0.25, 0), (0.2501, 1), (0.75, 2), (1.25, 2), (1.75, 4), (2.5, 4), (3.5, 6),
+                                    (5.0, 6), (5.001, 7), (6.0, 7), (0.5, 1), (3.0, 5)])
+def test_codes_round_to_nearest_ties_to_even(x, code):
+    block = torch.zeros(16, dtype=torch.float64)
+    block[0], block[1], block[2] = 6.0, x, -x     # the maximum 6 gives the scale 1
+    _, codes, byte = ref.quantise(block)
+    assert ref.SCALES[byte] == 1.0
+    assert codes[1] == code and codes[2] == (code | 8)
+
+
+def test_pack_and_unpack_agree():
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(2, 3, 128, 64, generator=g, dtype=torch.float64)
+    kv, kcode, kb = ref.quantise(x)
+    vv, vcode, vb = ref.quantise(x.flip(2))
+    k, v = ref.unpack(ref.pack(kcode, kb, vcode, vb))
+    assert torch.equal(k, kv) and torch.equal(v, vv)
+
+
+# ------------------------------------------------------------------- refusals
+P = 1 << 20   # a 16-byte aligned address that is never read
+
+
+def cache(**kw):
+    f = dict(k_codes=P, k_scales=P, v_codes=P, v_scales=P, batch=1, heads_kv=2, head_dim=128, capacity=256)
+    f.update(kw)
+    return CacheStruct(*[f[n] for n, _ in CacheStruct._fields_])
+
+
+def query(**kw):
+    f = dict(seqlen_q=1, heads_q=4, softmax_scale=0.0, rms_eps=1e-6, rope_batch_stride=0)
+    f.update(kw)
+    return QueryStruct(*[f[n] for n, _ in QueryStruct._fields_])
+
+
+BAD_CACHES = [(dict(k_codes=None), INVALID), (dict(v_scales=None), INVALID), (dict(batch=0), INVALID),
+              (dict(heads_kv=-1), INVALID), (dict(capacity=0), INVALID), (dict(head_dim=96), UNSUPPORTED),
+              (dict(capacity=200), UNSUPPORTED), (dict(k_codes=P + 8), INVALID), (dict(v_codes=P + 4), INVALID),
+              (dict(batch=40000), UNSUPPORTED)]
+
+
+def with_bad_cache(c):
+    """A call of each entry point with a cache that has to be refused (the
+    pointers must never be read: on a machine with a GPU that would fault)."""
+    lib = bca.library()
+    c = ctypes.byref(c) if c is not None else None
+    good = ctypes.byref(cache(k_codes=2 * P, k_scales=2 * P, v_codes=2 * P, v_scales=2 * P))
+    q = ctypes.byref(query())
+    return [lib.magi_bca_kv4_append(P, P, c, P, None, 1, None, 0, 1e-6, None),
+            lib.magi_bca_kv4_read(c, P, 1, P, P, None),
+            lib.magi_bca_kv4_fwd(P, c, P, P, P, None, None, None, P, P, P, 1 << 40, q, None),
+            lib.magi_bca_kv4_weights(P, c, P, P, P, P, None, P, 1.0, P, 1 << 40, q, None),
+            lib.magi_bca_kv4_evict(c, P, P, 1, 0, good, 2 * P, 2 * P, P, None)]
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_bad_caches_are_refused_by_every_entry_point(bad, status):
+    assert set(with_bad_cache(cache(**bad))) == {status}
+
+
+def test_a_null_cache_is_refused():
+    assert set(with_bad_cache(None)) == {INVALID}
+
+
+@pytest.mark.parametrize("bad,status", [(dict(seqlen_q=0), INVALID), (dict(heads_q=0), INVALID),
+                                        (dict(heads_q=5), UNSUPPORTED), (dict(rms_eps=-1.0), INVALID),
+                                        (dict(rms_eps=float("nan")), INVALID), (dict(softmax_scale=-1.0), INVALID),
+                                        (dict(softmax_scale=float("inf")), INVALID),
+                                        (dict(rope_batch_stride=-1), INVALID),
+                                        (dict(seqlen_q=1 << 30, heads_q=4), UNSUPPORTED)])
+def test_bad_queries_are_refused(bad, status):
+    lib, c, q = bca.library(), ctypes.byref(cache()), ctypes.byref(query(**bad))
+    assert lib.magi_bca_kv4_fwd(P, c, P, P, P, None, None, None, P, P, P, 1 << 40, q, None) == status
+    assert lib.magi_bca_kv4_weights(P, c, P, P, P, P, None, P, 1.0, P, 1 << 40, q, None) == status
+    for name in ("fwd", "weights"):
+        f = getattr(lib, f"magi_bca_kv4_{name}_workspace_size")
+        assert f(ctypes.byref(cache()), ctypes.byref(query(**bad))) == 0
+
+
+def test_append_and_read_arguments():
+    lib, c = bca.library(), ctypes.byref(cache())
+    ap = lambda k=P, v=P, start=P, n=1, stride=0, eps=1e-6: lib.magi_bca_kv4_append(  # noqa: E731
+        k, v, c, start, None, n, None, stride, eps, None)
+    assert ap(k=None) == ap(v=None) == ap(start=None) == ap(n=0) == ap(n=-3) == ap(stride=-1) == INVALID
+    assert ap(k=P + 2) == ap(v=P + 8) == ap(eps=-1.0) == ap(eps=float("inf")) == INVALID
+    rd = lambda k=P, v=P, n=1: lib.magi_bca_kv4_read(c, P, n, k, v, None)  # noqa: E731
+    assert rd(k=None) == rd(v=None) == rd(n=0) == rd(k=P + 2) == INVALID
+
+
+def test_fwd_and_weights_arguments():
+    lib, c, q = bca.library(), ctypes.byref(cache()), ctypes.byref(query())
+
+    def fwd(qp=P, ln=P, gq=P, gk=P, bo=None, bl=None, out=P, lse=P, ws=P, n=1 << 40, qq=q):
+        return lib.magi_bca_kv4_fwd(qp, c, ln, gq, gk, None, bo, bl, out, lse, ws, n, qq, None)
+
+    assert fwd(qp=None) == fwd(ln=None) == fwd(gq=None) == fwd(gk=None) == fwd(out=None) == fwd(qq=None) == INVALID
+    assert fwd(bo=2 * P) == fwd(bl=2 * P) == INVALID                     # one without the other
+    assert fwd(bo=P, bl=2 * P) == fwd(bo=2 * P, bl=P) == INVALID         # base in the outputs' place
+    assert fwd(qp=P + 2) == fwd(out=P + 8) == fwd(bo=2 * P + 8, bl=2 * P) == INVALID
+    big = ctypes.byref(query(seqlen_q=512))
+    need = lib.magi_bca_kv4_fwd_workspace_size(c, big)
+    assert need > 0
+    assert fwd(qq=big, n=need - 1) == TOO_SMALL
+    assert fwd(qq=big, ws=None) == fwd(qq=big, ws=P + 16) == INVALID
+
+    def wts(qp=P, ln=P, lse=P, w=P, decay=1.0, ws=P, n=1 << 40, qq=q):
+        return lib.magi_bca_kv4_weights(qp, c, ln, lse, P, P, None, w, decay, ws, n, qq, None)
+
+    assert wts(qp=None) == wts(ln=None) == wts(lse=None) == wts(w=None) == INVALID
+    assert wts(w=P + 4) == wts(decay=float("nan")) == INVALID
+    need = lib.magi_bca_kv4_weights_workspace_size(c, big)
+    assert need > 0 and wts(qq=big, n=need - 1) == TOO_SMALL
+
+
+def test_evict_arguments():
+    lib = bca.library()
+    a = cache()
+    b = dict(k_codes=2 * P, k_scales=2 * P, v_codes=2 * P, v_scales=2 * P)
+
+    def ev(w=P, ln=P, keep=8, recent=4, dw=2 * P, dl=2 * P, ix=P, **dst):
+        d = cache(**{**b, **dst})
+        return lib.magi_bca_kv4_evict(ctypes.byref(a), w, ln, keep, recent, ctypes.byref(d), dw, dl, ix, None)
+
+    assert ev(w=None) == ev(ln=None) == ev(dw=None) == ev(dl=None) == ev(ix=None) == INVALID
+    assert ev(keep=0) == ev(recent=-1) == ev(recent=9) == ev(keep=257) == INVALID
+    assert ev(batch=2) == ev(heads_kv=1) == ev(head_dim=64) == INVALID
+    assert ev(k_codes=P) == ev(k_scales=P) == ev(v_codes=P) == ev(v_scales=P) == ev(dw=P) == ev(dl=P) == INVALID
+
+
+def test_workspace_sizes():
+    lib = bca.library()
+    c = ctypes.byref(cache(batch=1, heads_kv=64, capacity=128))
+    # 64 heads of one part each: no parts to join, nothing to expand
+    assert lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(heads_q=64))) == 0
+    assert lib.magi_bca_kv4_weights_workspace_size(c, ctypes.byref(query(heads_q=64))) == 0
+    # a chunk: the expanded cache and queries at least
+    c = ctypes.byref(cache(batch=2, heads_kv=8, capacity=92160))
+    n = lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(seqlen_q=5760, heads_q=24)))
+    assert n >= 2 * 8 * 92160 * 128 * 2 * 2 + 2 * 24 * 5760 * 128 * 2
+
+
+def test_the_binding_refuses_cpu_tensors_and_bad_shapes():
+    c = bca.magi_bca_kv4_cache(1, 2, 64, 100, device="cpu")
+    assert c.k_codes.shape == (1, 2, 128, 32) and c.v_scales.shape == (1, 2, 64, 4, 2)
+    k = torch.zeros(1, 3, 2, 64, dtype=torch.bfloat16)
+    start = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        bca.magi_bca_kv4_append(c, k, k, start)
+    with pytest.raises(TypeError):
+        bca.magi_bca_kv4_read(c, start, 3)
+    with pytest.raises(TypeError):
+        bca.magi_bca_kv4_fwd(k, c, start, torch.ones(64), torch.ones(64))
+    with pytest.raises(TypeError):
+        bca.magi_bca_kv4_weights(k, c, start, torch.zeros(1, 2, 3), torch.ones(64), torch.ones(64), torch.zeros(1, 2, 128))
+    with pytest.raises(TypeError):
+        bca.magi_bca_kv4_evict(c, torch.zeros(1, 2, 128), start, 4, 0, c, torch.zeros(1, 2, 128))
+    with pytest.raises(ValueError):
+        bca.magi_bca_kv4_cache(1, 2, 80, 128, device="cpu")
+    with pytest.raises(ValueError):
+        bca.magi_bca_kv4_cache(0, 2, 64, 128, device="cpu")
