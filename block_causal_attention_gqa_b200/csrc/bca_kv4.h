@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -23,6 +24,27 @@ struct Cache {
   uint8_t* vs;   // [B, H, cap/2, D/16, 2]
   int batch, heads, dim, cap;
 };
+
+// Lets a kernel use `bytes` of dynamic shared memory; asked of the runtime once
+// for each device and growth (`have`: the kernel's record, zero-initialised).
+struct SmemRecord {
+  std::atomic<int> bytes[64];
+};
+
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, SmemRecord& have) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && have.bytes[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) {
+    int was = have.bytes[dev].load();
+    while (was < bytes && !have.bytes[dev].compare_exchange_weak(was, bytes)) {
+    }
+  }
+  return e;
+}
 
 struct AppendParams {
   Cache c;
@@ -60,9 +82,9 @@ struct FwdParams4 {
   float* lse;                 // or nullptr
   int heads_q, sq;
   float scale_log2, eps;
-  int n_splits;            // parts of a history that different CTAs read
-  float* part_o;           // [n_splits, B, H, G * Sq, D] fp32
-  float2* part_ml;         // [n_splits, B, H, G * Sq] (reference in log2 units, sum)
+  int n_splits;            // chunk path: parts of a history that different CTAs read
+  float* part_o;           // rows of D fp32: chunk path [n_splits, B, H, G * Sq], token path [slot, row of a tile]
+  float2* part_ml;         // for each such row (reference in log2 units, sum)
   uint16_t* qh;            // chunk path: folded queries [B, H, G * Sq, D] fp16 (high part)
   uint16_t* ql;            //   and low part (weights only)
   uint16_t* kx;            // chunk path: expanded keys [B, H, cap, D] fp16
@@ -88,12 +110,10 @@ struct EvictParams {
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_read(const ReadParams& p, cudaStream_t s);
 
-// Few query rows per key/value head: the rows of a head fit tiles of 8.
-constexpr int kTokenRows = 8;
-int token_splits(const Cache& c, int row_tiles);
+// Few query rows per key/value head: the rows in groups of 4, mma.sync.
+int64_t token_piece_rows(const Cache& c, int rows);   // rows of the fwd's part_o / part_ml
 cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s);
 cudaError_t launch_token_weights(const FwdParams4& p, cudaStream_t s);
-cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s);
 
 // Many rows: expanded fp16 operands and the tensor cores of tcgen05.
 int chunk_splits(const Cache& c, int rows);
@@ -103,6 +123,8 @@ cudaError_t launch_chunk_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const
                              cudaStream_t s);
 cudaError_t launch_chunk_weights(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk,
                                  const FwdParams4& p, cudaStream_t s);
+
+cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s);
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 

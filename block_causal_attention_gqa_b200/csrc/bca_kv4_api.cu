@@ -44,7 +44,7 @@ int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
 
 int rows_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q) { return q.heads_q / c.heads_kv * q.seqlen_q; }
 
-// Which kernels: the token kernels read the cache once for each 8 rows (fwd)
+// Which kernels: the token kernels convert the cache once for each 8 rows (fwd)
 // or once in all (weights), the chunk kernels expand it to fp16 first.
 constexpr int kTokenFwdRows = 32;
 constexpr int kTokenWeightRows = 64;
@@ -69,7 +69,11 @@ Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weig
   p.token = rows <= (weights ? kTokenWeightRows : kTokenFwdRows);
   p.rows_pad = (int)(((int64_t)rows + 127) / 128 * 128);
   if (p.token) {
-    p.splits = token_splits(cc, weights ? 1 : (rows + kTokenRows - 1) / kTokenRows);
+    if (!weights) {
+      const size_t n = (size_t)token_piece_rows(cc, rows);
+      p.part_o = take(n * D * 4);
+      p.part_ml = take(n * 8);
+    }
   } else {
     p.splits = weights ? chunk_weight_splits(cc, p.rows_pad) : chunk_splits(cc, rows);
     p.qh = take(BH * rows * D * 2);
@@ -81,11 +85,11 @@ Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weig
       p.vx = take(BH * c.capacity * D * 2);
     }
   }
-  if (p.splits > 1) {
+  if (!p.token && p.splits > 1) {
     if (!weights) {
       p.part_o = take((size_t)p.splits * BH * rows * D * 4);
       p.part_ml = take((size_t)p.splits * BH * rows * 8);
-    } else if (!p.token) {
+    } else {
       p.part_o = take((size_t)p.splits * BH * c.capacity * 4);
     }
   }
@@ -204,9 +208,8 @@ int magi_bca_kv4_fwd(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, co
   p.out = out;
   p.lse = lse;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (plan.token) {
-    st = done("cache attention launch", launch_token_fwd(p, cs));
-  } else {
+  if (plan.token) return done("cache attention launch", launch_token_fwd(p, cs));
+  {
     const int BH = cache->batch * cache->heads_kv, rows = rows_of(*cache, *query), D = cache->head_dim;
     CUtensorMap tq, tk, tv;
     if (make_tensor_map_bf16(&tq, p.qh, BH, rows, 1, D) != MAGI_BCA_OK ||
@@ -273,7 +276,7 @@ int magi_bca_kv4_evict(const magi_bca_kv4_cache* cache, const float* weights, co
   // tokens move while others are still read: source and destination are different memory
   if (dst_cache->k_codes == cache->k_codes || dst_cache->k_scales == cache->k_scales ||
       dst_cache->v_codes == cache->v_codes || dst_cache->v_scales == cache->v_scales || dst_weights == weights ||
-      dst_lengths == lengths)
+      dst_lengths == lengths || !aligned(weights, 16))
     return MAGI_BCA_INVALID_ARG;
   int* status;
   st = device_status_word(&status);

@@ -25,6 +25,7 @@
 // the tensor cores while the CUDA cores take 2^(s - lse), one MUFU operation a
 // pair, 1024 clocks a tile for either.
 #include <algorithm>
+#include <type_traits>
 
 #include "bca_kv4.cuh"
 #include "bca_kv4_query.cuh"
@@ -447,6 +448,38 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
+// Joins the parts of the rows: one warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_combine_kernel(const FwdParams4 p) {
+  constexpr int F = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int G = p.heads_q / p.c.heads, rows = G * p.sq;
+  const int64_t groups = (int64_t)p.c.batch * p.c.heads;
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= groups * rows) return;
+  const int64_t stride = groups * rows;
+  float mm = -INFINITY;
+  for (int s = lane; s < p.n_splits; s += 32) mm = fmaxf(mm, p.part_ml[s * stride + r].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  float acc[F] = {}, ll = 0.f;
+  if (mm != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < p.n_splits; ++s) {
+      const int64_t at = s * stride + r;
+      const float2 ml = p.part_ml[at];
+      if (ml.x == -INFINITY) continue;     // an empty part wrote no O
+      const float w = fast_exp2(ml.x - mm);
+      ll += ml.y * w;
+#pragma unroll
+      for (int f = 0; f < F; ++f) acc[f] = fmaf(p.part_o[at * D + lane * F + f], w, acc[f]);
+    }
+  }
+  const int bh = (int)(r / rows);
+  finish_row<F>(p, bh / p.c.heads, bh % p.c.heads, G, (int)(r % rows), D, lane * F, mm, ll, acc);
+}
+
 // ------------------------------------------------------------------ weights
 template <int D>
 struct WLayout {
@@ -636,8 +669,8 @@ cudaError_t expand_d(const FwdParams4& p, bool values, bool low, cudaStream_t s)
 template <int D>
 cudaError_t chunk_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
                         cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kv4_chunk_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdLayout<D>::kAlloc);
+  static SmemRecord have;
+  const cudaError_t e = allow_smem(kv4_chunk_fwd_kernel<D>, FwdLayout<D>::kAlloc, have);
   if (e != cudaSuccess) return e;
   const int rows = p.heads_q / p.c.heads * p.sq;
   const dim3 grid((rows + 255) / 256 * p.n_splits, p.c.batch * p.c.heads);
@@ -648,8 +681,8 @@ cudaError_t chunk_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 template <int D>
 cudaError_t chunk_weights_d(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk, const FwdParams4& p,
                             cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kv4_chunk_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       WLayout<D>::kAlloc);
+  static SmemRecord have;
+  cudaError_t e = allow_smem(kv4_chunk_weights_kernel<D>, WLayout<D>::kAlloc, have);
   if (e != cudaSuccess) return e;
   const int BH = p.c.batch * p.c.heads;
   kv4_chunk_weights_kernel<D><<<dim3(p.c.cap / 128, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s>>>(tqh, tql, tk, p);
@@ -683,6 +716,21 @@ cudaError_t launch_expand(const FwdParams4& p, bool values, bool low, cudaStream
 cudaError_t launch_chunk_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
                              cudaStream_t s) {
   return p.c.dim == 128 ? chunk_fwd_d<128>(tq, tk, tv, p, s) : chunk_fwd_d<64>(tq, tk, tv, p, s);
+}
+
+cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s) {
+  const int64_t rows = (int64_t)p.c.batch * p.heads_q * p.sq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return p.c.dim == 128 ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<128>, p)
+                        : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<64>, p);
 }
 
 cudaError_t launch_chunk_weights(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk,

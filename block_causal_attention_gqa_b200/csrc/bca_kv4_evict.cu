@@ -7,11 +7,12 @@
 // Selection (kv4_select_kernel).  A weight is mapped to an unsigned integer of
 // the same order and the need-th largest is found digit by digit (11, 11 and
 // 10 bits), a histogram of the candidates with the digits so far at each.  A
-// cluster of 8 CTAs shares a head: each counts an eighth, all read the eight
-// histograms through distributed shared memory, so nothing but the index
-// table goes through global memory.  The kept tokens are then numbered in
-// their order by ballots: a warp takes a contiguous run and starts at the
-// counts of the runs before it.
+// cluster of 8 CTAs shares a head: each keeps the keys of an eighth in shared
+// memory, counts them there and adds its counts that are not zero to the
+// totals of all eight through distributed shared memory (a few hundred bins;
+// reading all eight histograms whole took five times as long).  The kept
+// tokens are then numbered in their order by ballots: a warp takes a
+// contiguous run and starts at the counts of the runs before it.
 //
 // Moving (kv4_move_kernel).  Bound by bytes: a kept token is read and written
 // once.  A row of the value cache holds two tokens, so a destination row is
@@ -39,16 +40,21 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 
+constexpr int kSelKeys = 40 * 1024;   // keys a CTA keeps; longer runs are read again each time
+
 struct SelShared {
-  uint32_t hist[3][kBins];
+  uint32_t hist[kBins];      // this CTA's counts
+  uint32_t total[3][kBins];  // the cluster's
   uint32_t scan[kSelThreads / 32];
   uint32_t warp_gt[kSelThreads / 32], warp_eq[kSelThreads / 32];
   uint32_t cta_gt, cta_eq;
   uint32_t bin, above;
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictParams p) {
-  __shared__ SelShared sh;
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictParams p, bool held) {
+  extern __shared__ __align__(16) uint8_t sel_smem[];
+  SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelShared));
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -66,31 +72,37 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   // the need-th largest key and how many of those equal to it stay
   uint32_t top = need == 0 ? 0xffffffffu : 0u;   // all stay: every key is above or equal
   uint32_t ties = need == 0 ? 0u : 0x7fffffffu;
+  if (held)
+    for (int i = i0 + tid * 4; i < i1; i += kSelThreads * 4) {   // i0 and the row are multiples of 4 (or past n)
+      const float4 x = __ldg(reinterpret_cast<const float4*>(w + i));
+      *reinterpret_cast<uint4*>(keys + (i - i0)) = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+    }
+  auto key_at = [&](int i) { return held ? keys[i - i0] : order_key(__ldg(w + i)); };
   if (need > 0 && need < n) {                    // the same for the whole cluster
     uint32_t prefix = 0, left = (uint32_t)need;
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-    __syncthreads();
+    for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = sh.total[0][i] = sh.total[1][i] = sh.total[2][i] = 0;
+    cluster.sync();
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int bits = pass == 2 ? 10 : 11;
       for (int i = i0 + tid; i < i1; i += kSelThreads) {
-        const uint32_t key = order_key(__ldg(w + i));
-        if (pass == 0 || (key >> (shift + bits)) == prefix)
-          atomicAdd(&sh.hist[pass][(key >> shift) & ((1u << bits) - 1u)], 1u);
+        const uint32_t key = key_at(i);
+        if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&sh.hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      __syncthreads();
+      for (int i = tid; i < kBins; i += kSelThreads) {
+        const uint32_t v = sh.hist[i];
+        if (v == 0) continue;
+        sh.hist[i] = 0;
+        for (int r = 0; r < kCluster; ++r) atomicAdd(cluster.map_shared_rank(&sh.total[pass][i], r), v);
       }
       cluster.sync();
-      // thread t holds the counts of bins 4t .. 4t+3 from the top, over the cluster
+      // thread t holds the counts of bins 4t .. 4t+3 from the top
       constexpr int kPer = kBins / kSelThreads;
-      uint32_t cnt[kPer] = {}, mine = 0;
+      uint32_t cnt[kPer], mine = 0;
 #pragma unroll
-      for (int r = 0; r < kCluster; ++r) {
-        const uint32_t* h = cluster.map_shared_rank(&sh.hist[pass][0], r);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) cnt[k] += h[kBins - 1 - (tid * kPer + k)];
-      }
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) mine += cnt[k];
+      for (int k = 0; k < kPer; ++k) mine += cnt[k] = sh.total[pass][kBins - 1 - (tid * kPer + k)];
       uint32_t incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -115,6 +127,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
     }
     top = prefix;
     ties = left;
+  } else {
+    __syncthreads();
   }
 
   // number the kept tokens of this CTA's run, warp by warp
@@ -122,7 +136,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   const int a0 = min(i0 + warp * wseg, i1), a1 = min(a0 + wseg, i1);
   uint32_t gt = 0, eq = 0;
   for (int i = a0; i < a1; i += 32) {
-    const uint32_t key = i + lane < a1 ? order_key(__ldg(w + i + lane)) : 0u;
+    const uint32_t key = i + lane < a1 ? key_at(i + lane) : 0u;
     const bool in = i + lane < a1;
     gt += __popc(__ballot_sync(0xffffffffu, in && key > top));
     eq += __popc(__ballot_sync(0xffffffffu, in && key == top));
@@ -155,7 +169,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   const uint32_t below = (1u << lane) - 1u;
   for (int i = a0; i < a1; i += 32) {
     const bool in = i + lane < a1;
-    const uint32_t key = in ? order_key(__ldg(w + i + lane)) : 0u;
+    const uint32_t key = in ? key_at(i + lane) : 0u;
     const uint32_t mg = __ballot_sync(0xffffffffu, in && key > top);
     const uint32_t me = __ballot_sync(0xffffffffu, in && key == top);
     const uint32_t eq_rank = eq0 + __popc(me & below);
@@ -169,56 +183,105 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   if (rank == 0 && tid == 0 && bh % p.src.heads == 0) p.new_lengths[b] = kept;
 }
 
-// One warp per destination row of two tokens.
+// One warp per 16 destination tokens (8 value rows), so that each lane has some
+// hundred bytes under way.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_move_kernel(const EvictParams p) {
+  constexpr int kTok = 16;
+  constexpr int kK = D / 32;       // 16-byte pieces of a key row
+  constexpr int kV = D / 16;       // 16-byte pieces of a value row (two tokens)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / p.src.heads;
   const int kept = min(min(max(__ldg(p.lengths + b), 0), p.src.cap), p.keep);
-  const int pair = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (2 * pair >= kept) return;
-  const bool two = 2 * pair + 1 < kept;
-  const int32_t* index = p.index + (int64_t)bh * p.keep + 2 * pair;
-  const int s0 = index[0], s1 = two ? index[1] : s0;
-  const int64_t src = (int64_t)bh * p.src.cap, dst = (int64_t)bh * p.dst.cap + 2 * pair;
-  constexpr int kRow = D / 8;     // words of a key row
-  // keys: lanes [0, kRow) the first token, [kRow, 2 kRow) the second
-  if (lane < (two ? 2 * kRow : kRow)) {
-    const int64_t from = src + (lane < kRow ? s0 : s1);
-    const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(p.src.kc + from * (D / 2)) + lane % kRow);
-    (reinterpret_cast<uint32_t*>(p.dst.kc + dst * (D / 2)))[lane] = x;
+  const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kTok;
+  const int n = min(kTok, kept - t0);
+  if (n <= 0) return;
+  const int64_t src = (int64_t)bh * p.src.cap, dst = (int64_t)bh * p.dst.cap + t0;
+  // lane t (and t + 16): where token t of the sixteen comes from
+  const int from = p.index[(int64_t)bh * p.keep + t0 + min(lane & 15, n - 1)];   // not __ldg: written while this grid was starting
+  uint4 k[kK * kTok / 32], va[kV * kTok / 64], vb[kV * kTok / 64];
+#pragma unroll
+  for (int i = 0; i < kK * kTok / 32; ++i) {
+    const int piece = i * 32 + lane, t = piece / kK;
+    const int s = __shfl_sync(0xffffffffu, from, t);
+    k[i] = __ldg(reinterpret_cast<const uint4*>(p.src.kc + (src + s) * (D / 2)) + piece % kK);
   }
-  // values: D bytes, a half from each source row
-  if (lane < D / 4) {
-    const uint32_t x0 = __ldg(reinterpret_cast<const uint32_t*>(p.src.vc + (src / 2 + s0 / 2) * D) + lane);
-    const uint32_t x1 = __ldg(reinterpret_cast<const uint32_t*>(p.src.vc + (src / 2 + s1 / 2) * D) + lane);
-    uint32_t* to = reinterpret_cast<uint32_t*>(p.dst.vc + dst / 2 * D) + lane;
-    const uint32_t lo = (x0 >> (4 * (s0 & 1))) & 0x0f0f0f0fu, hi = (x1 >> (4 * (s1 & 1))) & 0x0f0f0f0fu;
-    *to = lo | (two ? hi << 4 : *to & 0xf0f0f0f0u);
+#pragma unroll
+  for (int i = 0; i < kV * kTok / 64; ++i) {
+    const int piece = i * 32 + lane, r = piece / kV;
+    const int s0 = __shfl_sync(0xffffffffu, from, 2 * r), s1 = __shfl_sync(0xffffffffu, from, 2 * r + 1);
+    va[i] = __ldg(reinterpret_cast<const uint4*>(p.src.vc + (src / 2 + s0 / 2) * D) + piece % kV);
+    vb[i] = __ldg(reinterpret_cast<const uint4*>(p.src.vc + (src / 2 + s1 / 2) * D) + piece % kV);
   }
-  // scales and weights
-  const int side = lane & 1, blk = lane >> 1;
-  if (side == 0 || two) {
-    const int s = side ? s1 : s0;
-    if (blk < D / 16) {
-      p.dst.ks[(dst + side) * (D / 16) + blk] = __ldg(p.src.ks + (src + s) * (D / 16) + blk);
-      p.dst.vs[(dst / 2 * (D / 16) + blk) * 2 + side] = __ldg(p.src.vs + ((src / 2 + s / 2) * (D / 16) + blk) * 2 + (s & 1));
+  // scales: lanes 0..15 a token's key and value scales each; lane t + 16 its weight
+  uint2 ks = make_uint2(0, 0);
+  uint4 vs = make_uint4(0, 0, 0, 0);
+  float w = 0.f;
+  if (lane < 16) {
+    if constexpr (D == 128) {
+      ks = __ldg(reinterpret_cast<const uint2*>(p.src.ks + (src + from) * 8));
+      vs = __ldg(reinterpret_cast<const uint4*>(p.src.vs + (src / 2 + from / 2) * 16));
+    } else {
+      ks.x = __ldg(reinterpret_cast<const uint32_t*>(p.src.ks + (src + from) * 4));
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(p.src.vs + (src / 2 + from / 2) * 8));
+      vs.x = y.x;
+      vs.y = y.y;
     }
-    if (blk == 15) p.w_dst[dst + side] = __ldg(p.w_src + src + s);
+  } else {
+    w = __ldg(p.w_src + src + from);
   }
+
+#pragma unroll
+  for (int i = 0; i < kK * kTok / 32; ++i) {
+    const int piece = i * 32 + lane;
+    if (piece / kK < n) reinterpret_cast<uint4*>(p.dst.kc + dst * (D / 2))[piece] = k[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kV * kTok / 64; ++i) {
+    const int piece = i * 32 + lane, r = piece / kV;
+    const int s0 = __shfl_sync(0xffffffffu, from, 2 * r), s1 = __shfl_sync(0xffffffffu, from, 2 * r + 1);
+    if (2 * r >= n) continue;
+    uint4* to = reinterpret_cast<uint4*>(p.dst.vc + dst / 2 * D) + piece;
+    const bool two = 2 * r + 1 < n;
+    const uint4 old = two ? make_uint4(0, 0, 0, 0) : *to;   // a half that no token takes stays
+    const int h0 = 4 * (s0 & 1), h1 = 4 * (s1 & 1);
+    auto join = [&](uint32_t a, uint32_t e, uint32_t o) {
+      const uint32_t lo = (a >> h0) & 0x0f0f0f0fu;
+      return two ? lo | (((e >> h1) & 0x0f0f0f0fu) << 4) : lo | (o & 0xf0f0f0f0u);
+    };
+    *to = make_uint4(join(va[i].x, vb[i].x, old.x), join(va[i].y, vb[i].y, old.y), join(va[i].z, vb[i].z, old.z),
+                     join(va[i].w, vb[i].w, old.w));
+  }
+  if (lane < n) {
+    uint8_t* to = p.dst.ks + (dst + lane) * (D / 16);
+    if constexpr (D == 128) *reinterpret_cast<uint2*>(to) = ks;
+    else *reinterpret_cast<uint32_t*>(to) = ks.x;
+    // the token's bytes of its source row (every second one) to every second byte of the destination row
+    const uint32_t x[4] = {vs.x, vs.y, vs.z, vs.w};
+    uint8_t* vt = p.dst.vs + (dst / 2 + lane / 2) * (D / 8) + (lane & 1);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) vt[2 * i] = (uint8_t)(x[i / 2] >> (16 * (i & 1) + 8 * (from & 1)));
+  }
+  if (lane >= 16 && lane - 16 < n) p.w_dst[dst + lane - 16] = w;
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   const int BH = p.src.batch * p.src.heads;
-  kv4_select_kernel<<<dim3(kCluster, BH), kSelThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  // room for the keys of an eighth of a full cache, if that is not too much
+  const int seg = (p.src.cap + kCluster * 32 - 1) / (kCluster * 32) * 32;
+  const int bytes = (int)sizeof(SelShared) + (seg <= kSelKeys ? seg * 4 : 0);
+  static SmemRecord have;
+  cudaError_t e = allow_smem(kv4_select_kernel, bytes, have);
+  if (e != cudaSuccess) return e;
+  kv4_select_kernel<<<dim3(kCluster, BH), kSelThreads, bytes, s>>>(p, seg <= kSelKeys);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int most = std::min(p.keep, p.src.cap);
-  cfg.gridDim = dim3((unsigned)(((most + 1) / 2 + 7) / 8), (unsigned)BH);
+  cfg.gridDim = dim3((unsigned)((most + 127) / 128), (unsigned)BH);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at;

@@ -52,20 +52,23 @@ __device__ __forceinline__ void fold_query(const FwdParams4& p, int b, int hk, i
   }
 }
 
-// The same into shared memory in the order of mma.m16n8k16's A fragments with
-// hi in rows 0..7 and lo in rows 8..15: 16 bytes {hi, lo, hi, lo} per (k-step
-// j, lane (g, c)), where lane c's features of k-step j are c D/4 + 4j .. + 3.
+// The same into shared memory in the order of mma.m16n8k16's B fragments, for
+// row `r` of a group of 4: column r is hi, column r + 4 lo, 8 bytes per (k-step
+// j, column, lane c), where lane c's features of k-step j are c D/4 + 4j .. + 3.
 template <int D>
 __device__ __forceinline__ void fold_query_fragment(const FwdParams4& p, int b, int hk, int G, int row, int rows,
-                                                    int g, int lane, uint8_t* smem_q) {
+                                                    int r, int lane, uint8_t* smem_q) {
   uint32_t hi[D / 64], lo[D / 64];
   fold_query<D>(p, b, hk, G, row, rows, lane, hi, lo);
   const int d = lane * (D / 32), c = d / (D / 4), j = d % (D / 4) / 4;
-  uint8_t* dst = smem_q + (j * 32 + g * 4 + c) * 16;
-  if constexpr (D == 128)
-    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], lo[0], hi[1], lo[1]);
-  else
-    *reinterpret_cast<uint2*>(dst + (d % 4) / 2 * 8) = make_uint2(hi[0], lo[0]);
+  uint8_t* dst = smem_q + (j * 32 + r * 4 + c) * 8;   // lo: 16 lanes on
+  if constexpr (D == 128) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(dst + 128) = make_uint2(lo[0], lo[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(dst + (d % 4) * 2) = hi[0];
+    *reinterpret_cast<uint32_t*>(dst + 128 + (d % 4) * 2) = lo[0];
+  }
 }
 
 // N words (1, 2 or a multiple of 4), in pieces of up to 16 bytes.

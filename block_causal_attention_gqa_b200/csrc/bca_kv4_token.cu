@@ -2,7 +2,7 @@
 // weight its keys receive (single tokens, short blocks of tokens).
 //
 // Mathematics.  The rows of a key/value head (group heads x queries) come in
-// tiles of 8.  With Q^ = q r_q gamma_q gamma_k scale log2(e) (rotated first),
+// groups of 4.  With Q^ = q r_q gamma_q gamma_k scale log2(e) (rotated first),
 //   s_ij = Q^_i . K^_j,  o_i = sum_j 2^(s_ij - m) v_j / sum_j 2^(s_ij - m)
 // with one pass over the history: a running reference m and sum per row.
 //
@@ -11,25 +11,32 @@
 // meets every row of the group), so the products are mma.m16n8k16 with fp16
 // operands, and all the work per value left to the CUDA cores is half a
 // conversion (e2m1x2 -> f16x2) and half a multiplication by the block's scale.
-//   - The cached values are exact in fp16.  The other operands are split in
-//     two fp16 numbers, x = hi + lo: the 8 rows fill M = 0..7 with hi and
-//     M = 8..15 with lo, so the split costs no more matrix instructions than a
-//     half-empty tile would, scores and sums are good to fp32's last bits, and
-//     a lane finds both parts of a product in its own accumulator.
+//   - Keys and values are the A operand (M = 16 tokens, or 16 features), the
+//     rows of the queries are N.  The cached values are exact in fp16; the
+//     other operand is split in two fp16 numbers, x = hi + lo, so that scores
+//     and sums are good to fp32's last bits: 4 rows fill N = 0..3 with hi and
+//     N = 4..7 with lo.  (With the rows as M the same products took twice the
+//     matrix instructions and twice the accumulators.)
 //   - The layouts of the fragments are met by renaming, not by moving data.
 //     The features of a dot product may be summed in any order, so lane c of a
-//     quad holds a contiguous quarter of a key row; and the columns of the
+//     quad holds a contiguous quarter of a key row; and the features of the
 //     second product may stand in any order, so lane group g holds a contiguous
 //     eighth of a value row, whose bytes hold two tokens each: a converted byte
 //     is a fragment register.  Every shared-memory read of a warp is one
-//     contiguous run.
+//     contiguous run.  Only P, a hundredth of the data, is transposed
+//     (movmatrix).
 //   - P is scaled by 2^7 (reference m - 7) and m moves only when a score passes
 //     it by 8, so P stays below 2^15 in fp16 and loses nothing above 2^-31.
 //   - Each warp streams its own steps of 32 tokens through its own ring of
 //     bulk copies (one lane issues, mbarriers complete), so warps do not wait
 //     for one another until the end.
-// A history is cut into n_splits parts for different CTAs; kv4_combine_kernel
-// joins their (m, l, O), launched early by programmatic dependent launch.
+//
+// Split.  The steps of all histories (batch element, head, row tile) are laid
+// end to end and cut into equal parts, one for each CTA of the grid, so
+// histories of any number and lengths keep every SM busy to the end.  A part of
+// one history is a piece; piece (CTA c, history h) has slot c + h of the
+// workspace, which no other has.  kv4_combine_kernel joins the pieces' (m, l,
+// O), launched early by programmatic dependent launch.
 #include <algorithm>
 
 #include "bca_kv4.cuh"
@@ -43,24 +50,25 @@ using namespace sm100;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kStep = 32;              // tokens of one step of a warp
 constexpr float kMove = 8.f;           // log2 units a score may pass the reference by
 constexpr float kLift = 7.f;           // P carries a factor 2^kLift
 
 enum : int { kErrRing = 3101, kErrRingW = 3102 };
 
-template <int D>
+// NT: row groups of 4 a CTA takes.
+template <int D, int NT>
 struct Ring {
+  static constexpr int kRows = 4 * NT;
   static constexpr int kKc = kStep * D / 2, kKs = kStep * D / 16, kVc = kStep / 2 * D, kVs = kStep * D / 16;
   static constexpr int kStage = kKc + kKs + kVc + kVs;
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int kQ = D / 16 * 32 * 16;             // query fragments of a row tile
+  static constexpr int kQ = NT * (D / 16) * 32 * 8;       // query fragments of a row tile
   static constexpr int kMergeRow = D + 4;                 // floats, padded
-  static constexpr int kMerge = kWarps * 8 * kMergeRow * 4;
+  static constexpr int kMerge = kWarps * kRows * kMergeRow * 4;
   static constexpr int kRing = kWarps * kWarp;
-  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;   // the merge reuses the ring
-  static constexpr int kTotal = kBody + kQ + kWarps * 8 * 8 + kWarps * kStages * 8;
+  static constexpr int kTotal = kRing + kMerge + kQ + kWarps * kRows * 8 + kWarps * kStages * 8 + 32;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -70,64 +78,142 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 8x8 fp16 transpose over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // Bounded wait whose outcome the whole warp agrees on.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
 }
 
-// Scores of 8 tokens (key rows kc, scales ks of the tile) against the row
-// tile: acc[0..1] the hi part of tokens 2c, 2c + 1 for row g, acc[2..3] the lo part.
+// A fragments of 16 tokens' keys (rows g and g + 8 of the tile; lane c's
+// quarter of the features): k-step j covers features c D/4 + 4j .. + 3.
 template <int D>
-__device__ __forceinline__ void score_tile(const uint8_t* kc, const uint8_t* ks, int g, int c,
-                                           const uint32_t (&q)[D / 16][4], float (&acc)[4]) {
-  uint32_t w[D / 32];
-  uint32_t sc[2];
-  if constexpr (D == 128) {
-    const uint4 x = *reinterpret_cast<const uint4*>(kc + g * 64 + c * 16);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    const uint32_t s2 = *reinterpret_cast<const uint16_t*>(ks + g * 8 + c * 2);
-    sc[0] = scale_dup(s2 & 0xffu);
-    sc[1] = scale_dup(s2 >> 8);
-  } else {
-    const uint2 x = *reinterpret_cast<const uint2*>(kc + g * 32 + c * 8);
-    w[0] = x.x; w[1] = x.y;
-    sc[0] = sc[1] = scale_dup(ks[g * 4 + c]);
-  }
+__device__ __forceinline__ void key_fragments(const uint8_t* kc, const uint8_t* ks, int g, int c,
+                                              uint32_t (&a)[D / 16][4]) {
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    uint32_t h[4];
-    codes_f16x8(w[i], h);
-    const uint32_t s = sc[i / 2];
-    mma16816(acc, q[2 * i], hmul2(h[0], s), hmul2(h[1], s));
-    mma16816(acc, q[2 * i + 1], hmul2(h[2], s), hmul2(h[3], s));
+  for (int r = 0; r < 2; ++r) {
+    const int tok = g + 8 * r;
+    uint32_t w[D / 32], sc[2];
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4*>(kc + tok * 64 + c * 16);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      const uint32_t s2 = *reinterpret_cast<const uint16_t*>(ks + tok * 8 + c * 2);
+      sc[0] = scale_dup(s2 & 0xffu);
+      sc[1] = scale_dup(s2 >> 8);
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(kc + tok * 32 + c * 8);
+      w[0] = x.x; w[1] = x.y;
+      sc[0] = sc[1] = scale_dup(ks[tok * 4 + c]);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t h[4];
+      codes_f16x8(w[i], h);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[2 * i + (k >> 1)][r + 2 * (k & 1)] = hmul2(h[k], sc[i / 2]);
+    }
   }
 }
 
+// Scores of 16 tokens against 4 rows, q the group's B fragments: x[0], x[1]
+// token g, x[2], x[3] token g + 8, rows 2(c & 1) and 2(c & 1) + 1 (lanes c and
+// c ^ 2 hold the same).
 template <int D>
-__device__ __forceinline__ void load_query_fragments(const uint8_t* smem_q, int lane, uint32_t (&q)[D / 16][4]) {
+__device__ __forceinline__ void score(const uint32_t (&a)[D / 16][4], const uint32_t (&q)[D / 16][2], float (&x)[4]) {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) mma16816(acc, a[j], q[j][0], q[j][1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = acc[i] + __shfl_xor_sync(0xffffffffu, acc[i], 2);   // hi + lo
+}
+
+template <int D>
+__device__ __forceinline__ void load_query_fragments(const uint8_t* smem_q, int lane, uint32_t (&q)[D / 16][2]) {
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
-    const uint4 x = *reinterpret_cast<const uint4*>(smem_q + (j * 32 + lane) * 16);
-    q[j][0] = x.x; q[j][1] = x.y; q[j][2] = x.z; q[j][3] = x.w;
+    const uint2 x = *reinterpret_cast<const uint2*>(smem_q + (j * 32 + lane) * 8);
+    q[j][0] = x.x; q[j][1] = x.y;
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 3) kv4_token_fwd_kernel(const FwdParams4 p) {
-  using R = Ring<D>;
+// ------------------------------------------------- histories laid end to end
+__device__ __forceinline__ int steps_of(const FwdParams4& p, int b) {
+  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  return (len + kStep - 1) / kStep;
+}
+
+// Steps of a batch element's one history, summed over the batch elements below
+// b and over all, by one warp.
+__device__ __forceinline__ void steps_below(const FwdParams4& p, int b, int lane, int64_t& below, int64_t& all) {
+  below = all = 0;
+  for (int i = lane; i < p.c.batch; i += 32) {
+    const int s = steps_of(p, i);
+    all += s;
+    if (i < b) below += s;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    below += __shfl_xor_sync(0xffffffffu, below, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+}
+
+// CTAs that get a part: no more than have a step for each warp.
+__device__ __forceinline__ int parts_of(int64_t all, int ctas) {
+  return (int)min((int64_t)ctas, (all + kWarps - 1) / kWarps);
+}
+
+// First flat step of CTA i's part (the end of the last one's for i >= parts_of).
+__device__ __forceinline__ int64_t part_begin(int64_t all, int i, int ctas) {
+  const int n = parts_of(all, ctas);
+  return i >= n ? all : all * i / n;
+}
+
+// Where the flat step x lies, by one warp: batch element, and the flat step its
+// first history begins at; `all` = steps of all histories.  per: histories of a
+// batch element.  x < all.
+__device__ __forceinline__ void locate(const FwdParams4& p, int64_t x, int per, int lane, int& b, int64_t& begin) {
+  begin = 0;
+  for (int i0 = 0; i0 < p.c.batch; i0 += 32) {
+    int64_t incl = i0 + lane < p.c.batch ? (int64_t)steps_of(p, i0 + lane) * per : 0;
+    const int64_t mine = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, begin + incl > x);
+    if (hit != 0) {
+      const int l = __ffs(hit) - 1;
+      b = i0 + l;
+      begin += __shfl_sync(0xffffffffu, incl - mine, l);
+      return;
+    }
+    begin += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  b = p.c.batch;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kernel(const FwdParams4 p) {
+  using R = Ring<D, NT>;
+  constexpr int kRows = R::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* smem_q = smem + R::kBody;
+  float* smem_merge = reinterpret_cast<float*>(smem + R::kRing);
+  uint8_t* smem_q = smem + R::kRing + R::kMerge;
   float2* smem_ml = reinterpret_cast<float2*>(smem_q + R::kQ);            // [warp][row]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_ml + kWarps * 8);     // [warp][stage]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_ml + kWarps * kRows); // [warp][stage]
+  int64_t* where = reinterpret_cast<int64_t*>(bars + kWarps * kStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, row0 = blockIdx.y * kTokenRows, bh = blockIdx.z;
-  const int b = bh / p.c.heads, hk = bh % p.c.heads;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
-  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
-  const int steps = (len + kStep - 1) / kStep;
-  const int s_begin = (int)((int64_t)steps * split / p.n_splits);
-  const int s_end = (int)((int64_t)steps * (split + 1) / p.n_splits);
+  const int row_tiles = (rows + kRows - 1) / kRows;
+  const int per = p.c.heads * row_tiles;                 // histories of a batch element
   uint8_t* ring = smem + warp * R::kWarp;
   uint64_t* bar = bars + warp * kStages;
 
@@ -135,340 +221,488 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_token_fwd_kernel(const FwdPar
     for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
     fence_mbar_init();
   }
-  __syncwarp();
-  const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
-  auto issue = [&](int k) {   // by lane 0
-    const int64_t tok = (int64_t)(s_begin + warp + k * kWarps) * kStep;
-    const int64_t at = (int64_t)bh * p.c.cap + tok;
-    uint8_t* dst = ring + (k % kStages) * R::kStage;
-    uint64_t* bb = bar + k % kStages;
-    mbar_arrive_expect_tx(bb, R::kStage);
-    bulk_load(dst, p.c.kc + at * (D / 2), R::kKc, bb);
-    bulk_load(dst + R::kKc, p.c.ks + at * (D / 16), R::kKs, bb);
-    bulk_load(dst + R::kKc + R::kKs, p.c.vc + at / 2 * D, R::kVc, bb);
-    bulk_load(dst + R::kKc + R::kKs + R::kVc, p.c.vs + at * (D / 16), R::kVs, bb);
-  };
-  if (lane == 0)
-    for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
-
-  // the row tile's queries, while the first copies are under way
-  for (int i = warp; i < kTokenRows; i += kWarps)
-    fold_query_fragment<D>(p, b, hk, G, row0 + i, rows, i, lane, smem_q);
+  if (warp == 0) {
+    int64_t none, all;
+    steps_below(p, 0, lane, none, all);
+    all *= per;
+    const int64_t x0 = part_begin(all, blockIdx.x, gridDim.x), x1 = part_begin(all, blockIdx.x + 1, gridDim.x);
+    int b = 0;
+    int64_t begin = 0;
+    if (x0 < x1) locate(p, x0, per, lane, b, begin);
+    if (lane == 0) {
+      where[0] = x0;
+      where[1] = x1;
+      where[2] = begin;
+      where[3] = b;
+    }
+  }
   __syncthreads();
-  uint32_t q[D / 16][4];
-  load_query_fragments<D>(smem_q, lane, q);
+  int64_t x = where[0];
+  const int64_t x1 = where[1];
+  int64_t begin = where[2];     // flat step where batch element b begins
+  int b = (int)where[3];
+  uint32_t it = 0;              // steps this warp has begun, over all pieces
 
-  float o[D / 8][4];
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  bool ok = true;
-  for (int k = 0; k < n_steps; ++k) {
-    ok = warp_wait(bar + k % kStages, (k / kStages) & 1, p.status, kErrRing);
-    if (!ok) break;
-    const uint8_t* kc = ring + (k % kStages) * R::kStage;
-    const uint8_t* ks = kc + R::kKc;
-    const uint8_t* vc = ks + R::kKs;
-    const uint8_t* vs = vc + R::kVc;
-    const int tok = (s_begin + warp + k * kWarps) * kStep;
-    float x[4][2];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      score_tile<D>(kc + t * 8 * (D / 2), ks + t * 8 * (D / 16), g, c, q, acc);
-      x[t][0] = acc[0] + acc[2];
-      x[t][1] = acc[1] + acc[3];
+  while (x < x1) {              // one piece: steps [s_begin, s_end) of one history
+    const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+    const int steps = (len + kStep - 1) / kStep;
+    if (steps == 0 || x >= begin + (int64_t)steps * per) {   // on to the next batch element
+      begin += (int64_t)steps * per;
+      ++b;
+      continue;
     }
-    const bool tail = tok + kStep > len;
-    if (tail) {
+    const int hist = (int)((x - begin) / steps);             // (head, row tile)
+    const int hk = hist / row_tiles, row0 = hist % row_tiles * kRows;
+    const int bh = b * p.c.heads + hk;
+    const int s_begin = (int)((x - begin) % steps);
+    const int s_end = (int)min((int64_t)steps, s_begin + (x1 - x));
+    const int64_t slot = (int64_t)blockIdx.x + (int64_t)b * per + hist;
+    x += s_end - s_begin;
+
+    const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
+    auto issue = [&](int k) {   // by lane 0
+      const int64_t at = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp + k * kWarps) * kStep;
+      const uint32_t st = (it + k) % kStages;
+      uint8_t* dst = ring + st * R::kStage;
+      uint64_t* bb = bar + st;
+      mbar_arrive_expect_tx(bb, R::kStage);
+      bulk_load(dst, p.c.kc + at * (D / 2), R::kKc, bb);
+      bulk_load(dst + R::kKc, p.c.ks + at * (D / 16), R::kKs, bb);
+      bulk_load(dst + R::kKc + R::kKs, p.c.vc + at / 2 * D, R::kVc, bb);
+      bulk_load(dst + R::kKc + R::kKs + R::kVc, p.c.vs + at * (D / 16), R::kVs, bb);
+    };
+    if (lane == 0)
+      for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
+
+    // the row tile's queries, while the first copies are under way
+    for (int i = warp; i < kRows; i += kWarps)
+      fold_query_fragment<D>(p, b, hk, G, row0 + i, rows, i & 3, lane, smem_q + (i >> 2) * (D / 16) * 32 * 8);
+    __syncthreads();
+    uint32_t q[NT][D / 16][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < NT; ++t) load_query_fragments<D>(smem_q + t * (D / 16) * 32 * 8, lane, q[t]);
+
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (tok + t * 8 + 2 * c + i >= len) x[t][i] = -INFINITY;
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
     }
-    const float top = fmaxf(fmax3(fmaxf(x[0][0], x[0][1]), x[1][0], x[1][1]),
-                            fmax3(fmaxf(x[2][0], x[2][1]), x[3][0], x[3][1]));
-    if (__any_sync(0xffffffffu, top > m + kMove)) {
-      float t = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      const float m1 = fmaxf(m, t);
-      const float alpha = m1 == -INFINITY ? 1.f : fast_exp2(m - m1);
-      m = m1;
-      l *= alpha;
+    bool ok = true;
+    for (int k = 0; k < n_steps; ++k) {
+      const uint32_t st = (it + k) % kStages;
+      ok = warp_wait(bar + st, ((it + k) / kStages) & 1, p.status, kErrRing);
+      if (!ok) break;
+      const uint8_t* kc = ring + st * R::kStage;
+      const uint8_t* ks = kc + R::kKc;
+      const uint8_t* vc = ks + R::kKs;
+      const uint8_t* vs = vc + R::kVc;
+      const int tok = (s_begin + warp + k * kWarps) * kStep;
+      const bool tail = tok + kStep > len;
+      float s[NT][2][4];
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
+      for (int u = 0; u < 2; ++u) {
+        uint32_t a[D / 16][4];
+        key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][i] *= alpha;
-    }
-    const float shift = m == -INFINITY ? 0.f : kLift - m;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float p0 = fast_exp2(x[t][0] + shift), p1 = fast_exp2(x[t][1] + shift);
-      l += p0 + p1;
-      hi[t] = pack_f16x2(p0, p1);
-      const float2 back = __half22float2(*reinterpret_cast<__half2*>(&hi[t]));
-      lo[t] = pack_f16x2(p0 - back.x, p1 - back.y);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t a[4] = {hi[2 * u], lo[2 * u], hi[2 * u + 1], lo[2 * u + 1]};
-      uint32_t v[2][D / 32], sc[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 8 * u + 4 * i + c;    // tokens 2 row, 2 row + 1 of the step
-        const uint8_t* src = vc + row * D + g * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(src);
-          v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(src);
-          v[i][0] = w.x; v[i][1] = w.y;
-        }
-        const uint32_t s2 = *reinterpret_cast<const uint16_t*>(vs + (row * (D / 16) + g * (D / 8) / 16) * 2);
-        sc[i] = scale_pair(s2 & 0xffu, s2 >> 8);
-        if (tail) {   // rows behind the end may hold anything: their values count as zero
-          if (tok + 2 * row >= len) sc[i] = 0u;
-          else if (tok + 2 * row + 1 >= len) sc[i] &= 0xffffu;
+        for (int t = 0; t < NT; ++t) {
+          score<D>(a, q[t], s[t][u]);
+          if (tail) {
+            if (tok + u * 16 + g >= len) s[t][u][0] = s[t][u][1] = -INFINITY;
+            if (tok + u * 16 + g + 8 >= len) s[t][u][2] = s[t][u][3] = -INFINITY;
+          }
         }
       }
+      uint32_t pb[NT][2][2];   // P as B fragments: [group][16 tokens][8 tokens]
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t h0[4], h1[4];
-        codes_f16x8(v[0][i], h0);
-        codes_f16x8(v[1][i], h1);
+      for (int t = 0; t < NT; ++t) {
+        float top[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma16816(o[4 * i + j], a, hmul2(h0[j], sc[0]), hmul2(h1[j], sc[1]));
+        for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmax3(s[t][0][r], s[t][0][r + 2], s[t][1][r]), s[t][1][r + 2]);
+        if (__any_sync(0xffffffffu, top[0] > m[t][0] + kMove || top[1] > m[t][1] + kMove)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], i));
+            const float m1 = fmaxf(m[t][r], top[r]);
+            const float alpha = m1 == -INFINITY ? 1.f : fast_exp2(m[t][r] - m1);
+            m[t][r] = m1;
+            l[t][r] *= alpha;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[t][j][r] *= alpha;
+              o[t][j][r + 2] *= alpha;
+            }
+          }
+        }
+        const float shift0 = m[t][0] == -INFINITY ? 0.f : kLift - m[t][0];
+        const float shift1 = m[t][1] == -INFINITY ? 0.f : kLift - m[t][1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float p0 = fast_exp2(s[t][u][2 * h] + shift0), p1 = fast_exp2(s[t][u][2 * h + 1] + shift1);
+            l[t][0] += p0;
+            l[t][1] += p1;
+            const uint32_t hi = pack_f16x2(p0, p1);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            const uint32_t lo = pack_f16x2(p0 - back.x, p1 - back.y);
+            pb[t][u][h] = transpose8(c < 2 ? hi : lo);
+          }
       }
-    }
-    __syncwarp();
-    if (lane == 0 && k + kStages < n_steps) issue(k + kStages);
-  }
-  // join the warps: every issued copy has been waited for, so the ring is free
-  if (__syncthreads_or(!ok)) return;
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-  // scores that are NaN (a query that is) leave the reference at -inf: they must not pass for an empty row
-  if (m == -INFINITY && !(l == 0.f)) m = kLift;
-  float* merge = reinterpret_cast<float*>(smem) + warp * 8 * R::kMergeRow + g * R::kMergeRow;
 #pragma unroll
-  for (int j = 0; j < D / 8; j += 4) {
-    float4 a, e;
-    a.x = o[j][0] + o[j][2]; a.y = o[j + 1][0] + o[j + 1][2]; a.z = o[j + 2][0] + o[j + 2][2]; a.w = o[j + 3][0] + o[j + 3][2];
-    e.x = o[j][1] + o[j][3]; e.y = o[j + 1][1] + o[j + 1][3]; e.z = o[j + 2][1] + o[j + 2][3]; e.w = o[j + 3][1] + o[j + 3][3];
-    *reinterpret_cast<float4*>(merge + 2 * c * (D / 8) + j) = a;
-    *reinterpret_cast<float4*>(merge + (2 * c + 1) * (D / 8) + j) = e;
-  }
-  if (c == 0) smem_ml[warp * 8 + g] = make_float2(m == -INFINITY ? -INFINITY : m - kLift, l);
-  __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      for (int u = 0; u < 2; ++u) {
+        uint32_t v[2][D / 32], sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * u + 4 * i + c;    // tokens 2 row, 2 row + 1 of the step
+          const uint8_t* src = vc + row * D + g * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src);
+            v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(src);
+            v[i][0] = w.x; v[i][1] = w.y;
+          }
+          const uint32_t s2 = *reinterpret_cast<const uint16_t*>(vs + (row * (D / 16) + g * (D / 8) / 16) * 2);
+          sc[i] = scale_pair(s2 & 0xffu, s2 >> 8);
+          if (tail) {   // rows behind the end may hold anything: their values count as zero
+            if (tok + 2 * row >= len) sc[i] = 0u;
+            else if (tok + 2 * row + 1 >= len) sc[i] &= 0xffffu;
+          }
+        }
+        // feature tile j: row g of A is feature g D/8 + 2j, row g + 8 the next
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t h0[4], h1[4];
+          codes_f16x8(v[0][i], h0);
+          codes_f16x8(v[1][i], h1);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {hmul2(h0[2 * j], sc[0]), hmul2(h0[2 * j + 1], sc[0]), hmul2(h1[2 * j], sc[1]),
+                                   hmul2(h1[2 * j + 1], sc[1])};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(o[t][2 * i + j], a, pb[t][u][0], pb[t][u][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && k + kStages < n_steps) issue(k + kStages);
+    }
+    it += n_steps;
+    // every issued copy has been waited for; a wait that failed ends the CTA
+    if (__syncthreads_or(!ok)) return;
 
-  // 16 threads a row, D / 16 features each
-  constexpr int F = D / 16;
-  const int i = threadIdx.x >> 4, f0 = (threadIdx.x & 15) * F;
-  const int row = row0 + i;
-  float mm = -INFINITY;
+    // join the warps
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, smem_ml[w * 8 + i].x);
-  float acc[F] = {}, ll = 0.f;
-  if (mm != -INFINITY) {
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = smem_ml[w * 8 + i];
-      const float s = fast_exp2(ml.x - mm);
-      ll += ml.y * s;
-      const float* src = reinterpret_cast<const float*>(smem) + (w * 8 + i) * R::kMergeRow + f0;
+      for (int r = 0; r < 2; ++r) {
 #pragma unroll
-      for (int f = 0; f < F; ++f) acc[f] = fmaf(src[f], s, acc[f]);
+        for (int i = 4; i < 32; i <<= 1) l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], i);
+        // scores that are NaN (a query that is) leave the reference at -inf: they must not pass for an empty row
+        if (m[t][r] == -INFINITY && !(l[t][r] == 0.f)) m[t][r] = kLift;
+      }
+      // hi + lo; lanes c < 2 then write row 2c, the others row 2(c - 2) + 1
+      const int own = c >> 1, row = 4 * t + 2 * (c & 1) + own;
+      float* dst = smem_merge + (warp * kRows + row) * R::kMergeRow + g * (D / 8);
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 2) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // features 2j .. 2j + 3 of the lane group's eighth
+          const float a0 = o[t][j + (e >> 1)][2 * (e & 1)], a1 = o[t][j + (e >> 1)][2 * (e & 1) + 1];
+          const float b0 = a0 + __shfl_xor_sync(0xffffffffu, a0, 2), b1 = a1 + __shfl_xor_sync(0xffffffffu, a1, 2);
+          f[e] = own ? b1 : b0;
+        }
+        *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(f[0], f[1], f[2], f[3]);
+      }
+      if (g == 0) smem_ml[warp * kRows + row] = make_float2((own ? m[t][1] : m[t][0]) - kLift, own ? l[t][1] : l[t][0]);
     }
-  }
-  if (row >= rows) return;
-  if (p.n_splits > 1) {
-    const int64_t at = ((int64_t)split * gridDim.z + bh) * rows + row;
-    if ((threadIdx.x & 15) == 0) p.part_ml[at] = make_float2(mm, ll);
+    __syncthreads();
+
+    constexpr int kPerRow = kThreads / kRows;            // threads a row
+    constexpr int F = D / kPerRow;                       // features a thread: 4 or 8 (2 at head_dim 64 of 4 rows)
+    const int i = threadIdx.x / kPerRow, f0 = threadIdx.x % kPerRow * F;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, smem_ml[w * kRows + i].x);
+    float acc[F] = {}, ll = 0.f;
     if (mm != -INFINITY) {
 #pragma unroll
-      for (int f = 0; f < F; f += 4)
-        *reinterpret_cast<float4*>(p.part_o + at * D + f0 + f) = make_float4(acc[f], acc[f + 1], acc[f + 2], acc[f + 3]);
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = smem_ml[w * kRows + i];
+        const float sc = fast_exp2(ml.x - mm);
+        ll += ml.y * sc;
+        const float* src = smem_merge + (w * kRows + i) * R::kMergeRow + f0;
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[f] = fmaf(src[f], sc, acc[f]);
+      }
     }
-  } else {
-    finish_row<F>(p, b, hk, G, row, D, f0, mm, ll, acc);
+    const int64_t at = slot * kRows + i;
+    if (f0 == 0) p.part_ml[at] = make_float2(mm, ll);
+#pragma unroll
+    for (int f = 0; f < F; f += 2)
+      *reinterpret_cast<float2*>(p.part_o + at * D + f0 + f) = make_float2(acc[f], acc[f + 1]);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the parts of the rows: one warp a row.
+// Joins the pieces of the rows: one CTA a row, its warps every eighth piece.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const FwdParams4 p) {
-  constexpr int F = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(256) kv4_token_combine_kernel(const FwdParams4 p, int kRows, int ctas) {
+  constexpr int F = D / 32, W = 8;
+  __shared__ float sm[W], sl[W];
+  __shared__ float so[W][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
-  const int64_t groups = (int64_t)p.c.batch * p.c.heads;
-  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= groups * rows) return;
-  const int64_t stride = groups * rows;
-  float mm = -INFINITY;
-  for (int s = lane; s < p.n_splits; s += 32) mm = fmaxf(mm, p.part_ml[s * stride + r].x);
+  const int row_tiles = (rows + kRows - 1) / kRows, per = p.c.heads * row_tiles;
+  const int bh = (int)(blockIdx.x / rows), row = (int)(blockIdx.x % rows);
+  const int b = bh / p.c.heads, hk = bh % p.c.heads;
+  int64_t below, all;
+  steps_below(p, b, lane, below, all);
+  const int steps = steps_of(p, b), hist = hk * row_tiles + row / kRows;
+  int n = 0;
+  int64_t slot = 0;
+  if (steps > 0) {
+    // the parts that hold a step of [x0, x1)
+    all *= per;
+    const int parts = parts_of(all, ctas);
+    const int64_t x0 = below * per + (int64_t)hist * steps, x1 = x0 + steps;
+    int c0 = (int)(x0 * parts / all), c1 = (int)((x1 * parts + all - 1) / all);
+    while (all * (c0 + 1) / parts <= x0) ++c0;
+    while (all * (c1 - 1) / parts >= x1) --c1;
+    slot = ((int64_t)b * per + hist + c0) * kRows + row % kRows;
+    n = c1 - c0;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float mm = -INFINITY, ll = 0.f;
+  float acc[F] = {};
+  for (int s0 = warp; s0 < n; s0 += 4 * W) {   // four pieces at a time
+    float2 ml[4];
+    float o[4][F];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  float acc[F] = {}, ll = 0.f;
-  if (mm != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < p.n_splits; ++s) {
-      const int64_t at = s * stride + r;
-      const float2 ml = p.part_ml[at];
-      if (ml.x == -INFINITY) continue;     // an empty part wrote no O
-      const float w = fast_exp2(ml.x - mm);
-      ll += ml.y * w;
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * W;
+      const int64_t at = slot + (int64_t)min(s, n - 1) * kRows;
+      ml[i] = p.part_ml[at];
+      if (s >= n) ml[i].x = -INFINITY;
 #pragma unroll
-      for (int f = 0; f < F; ++f) acc[f] = fmaf(p.part_o[at * D + lane * F + f], w, acc[f]);
+      for (int f = 0; f < F; ++f) o[i][f] = p.part_o[at * D + lane * F + f];
+    }
+    const float m1 = fmaxf(mm, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+    if (m1 == -INFINITY) continue;
+    const float keep = fast_exp2(mm - m1);
+    mm = m1;
+    ll *= keep;
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[f] *= keep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ml[i].x == -INFINITY) continue;
+      const float w = fast_exp2(ml[i].x - m1);
+      ll = fmaf(ml[i].y, w, ll);
+#pragma unroll
+      for (int f = 0; f < F; ++f) acc[f] = fmaf(o[i][f], w, acc[f]);
     }
   }
-  const int bh = (int)(r / rows);
-  finish_row<F>(p, bh / p.c.heads, bh % p.c.heads, G, (int)(r % rows), D, lane * F, mm, ll, acc);
+  if (n > 1) {   // the same for the whole CTA
+    if (lane == 0) {
+      sm[warp] = mm;
+      sl[warp] = ll;
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f) so[warp][lane * F + f] = acc[f];
+    __syncthreads();
+    if (warp != 0) return;
+    float m1 = -INFINITY;
+    const int used = min(n, W);
+    for (int w = 0; w < used; ++w) m1 = fmaxf(m1, sm[w]);
+    ll = 0.f;
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[f] = 0.f;
+    if (m1 != -INFINITY)
+      for (int w = 0; w < used; ++w) {
+        const float x = fast_exp2(sm[w] - m1);
+        ll = fmaf(sl[w], x, ll);
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[f] = fmaf(so[w][lane * F + f], x, acc[f]);
+      }
+    mm = m1;
+  }
+  if (warp == 0) finish_row<F>(p, b, hk, G, row, D, lane * F, mm, ll, acc);
 }
 
 // ------------------------------------------------------------------ weights
 //
 // w_j <- decay w_j + sum_i 2^(s_ij - lse_i log2 e): keys only.  A warp
-// converts a step's 32 keys once and holds them as fragments while the row
-// tiles pass, so any number of rows reads the cache once.
+// converts 16 keys once and holds them as fragments while the row groups
+// pass, so any number of rows reads the cache once.
 template <int D>
 struct RingW {
   static constexpr int kKc = kStep * D / 2, kKs = kStep * D / 16, kW = kStep * 4;
   static constexpr int kStage = kKc + kKs + kW;
-  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kStagesW = 3;
+  static constexpr int kWarp = kStagesW * kStage;
   static constexpr int kRing = kWarps * kWarp;
-  static constexpr int kTileQ = D / 16 * 32 * 16 + 8 * 4;   // fragments, then the 8 rows' lse in log2 units
-  static constexpr int bytes(int tiles) { return kRing + tiles * kTileQ + kWarps * kStages * 8; }
+  static constexpr int kGroupQ = D / 16 * 32 * 8 + 4 * 4;   // fragments, then the 4 rows' -lse in log2 units
+  static constexpr int bytes(int groups) { return kRing + groups * kGroupQ + kWarps * kStagesW * 8 + 32; }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_token_weights_kernel(const FwdParams4 p, int tiles) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const FwdParams4 p, int groups) {
   using R = RingW<D>;
+  constexpr int S = R::kStagesW;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + R::kRing);
-  uint8_t* smem_q = smem + R::kRing + kWarps * kStages * 8;
+  int64_t* where = reinterpret_cast<int64_t*>(bars + kWarps * S);
+  uint8_t* smem_q = smem + R::kRing + kWarps * S * 8 + 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int bh = blockIdx.y, b = bh / p.c.heads, hk = bh % p.c.heads;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
-  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
-  const int steps = (len + kStep - 1) / kStep;
-  const int s_begin = (int)((int64_t)steps * blockIdx.x / p.n_splits);
-  const int s_end = (int)((int64_t)steps * (blockIdx.x + 1) / p.n_splits);
   uint8_t* ring = smem + warp * R::kWarp;
-  uint64_t* bar = bars + warp * kStages;
+  uint64_t* bar = bars + warp * S;
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
+    for (int i = 0; i < S; ++i) mbar_init(bar + i, 1);
     fence_mbar_init();
   }
-  __syncwarp();
-  const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
-  const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
-  auto issue = [&](int k) {
-    const int64_t at = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp + k * kWarps) * kStep;
-    uint8_t* dst = ring + (k % kStages) * R::kStage;
-    uint64_t* bb = bar + k % kStages;
-    mbar_arrive_expect_tx(bb, R::kKc + R::kKs + (add ? R::kW : 0));
-    bulk_load(dst, p.c.kc + at * (D / 2), R::kKc, bb);
-    bulk_load(dst + R::kKc, p.c.ks + at * (D / 16), R::kKs, bb);
-    if (add) bulk_load(dst + R::kKc + R::kKs, p.weights + at, R::kW, bb);
-  };
-  if (lane == 0)
-    for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
-  for (int i = warp; i < tiles * kTokenRows; i += kWarps) {
-    uint8_t* tile = smem_q + (i >> 3) * R::kTileQ;
-    fold_query_fragment<D>(p, b, hk, G, i, rows, i & 7, lane, tile);
+  if (warp == 0) {
+    int64_t none, all;
+    steps_below(p, 0, lane, none, all);
+    all *= p.c.heads;
+    const int64_t x0 = part_begin(all, blockIdx.x, gridDim.x), x1 = part_begin(all, blockIdx.x + 1, gridDim.x);
+    int b = 0;
+    int64_t begin = 0;
+    if (x0 < x1) locate(p, x0, p.c.heads, lane, b, begin);
     if (lane == 0) {
-      // a row that saw nothing (lse = -inf) and rows behind the last give no weight
-      float x = INFINITY;
-      if (i < rows) x = p.w_lse[((int64_t)b * p.heads_q + hk * G + i / p.sq) * p.sq + i % p.sq] * kLog2e;
-      reinterpret_cast<float*>(tile + D / 16 * 32 * 16)[i & 7] = x == -INFINITY ? INFINITY : x;
+      where[0] = x0;
+      where[1] = x1;
+      where[2] = begin;
+      where[3] = b;
     }
   }
   __syncthreads();
-  for (int k = 0; k < n_steps; ++k) {
-    if (!warp_wait(bar + k % kStages, (k / kStages) & 1, p.status, kErrRingW)) break;
-    const uint8_t* kc = ring + (k % kStages) * R::kStage;
-    const uint8_t* ks = kc + R::kKc;
-    const int tok = (s_begin + warp + k * kWarps) * kStep;
-    float sum[4][2] = {};
-    for (int t0 = 0; t0 < tiles; ++t0) {
-      const uint8_t* tile = smem_q + t0 * R::kTileQ;
-      uint32_t q[D / 16][4];
-      load_query_fragments<D>(tile, lane, q);
-      const float neg = -reinterpret_cast<const float*>(tile + D / 16 * 32 * 16)[g];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        score_tile<D>(kc + t * 8 * (D / 2), ks + t * 8 * (D / 16), g, c, q, acc);
-        sum[t][0] += fast_exp2(acc[0] + acc[2] + neg);
-        sum[t][1] += fast_exp2(acc[1] + acc[3] + neg);
+  int64_t x = where[0];
+  const int64_t x1 = where[1];
+  int64_t begin = where[2];
+  int b = (int)where[3];
+  uint32_t it = 0;
+  const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
+
+  while (x < x1) {
+    const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+    const int steps = (len + kStep - 1) / kStep;
+    if (steps == 0 || x >= begin + (int64_t)steps * p.c.heads) {
+      begin += (int64_t)steps * p.c.heads;
+      ++b;
+      continue;
+    }
+    const int hk = (int)((x - begin) / steps), bh = b * p.c.heads + hk;
+    const int s_begin = (int)((x - begin) % steps);
+    const int s_end = (int)min((int64_t)steps, s_begin + (x1 - x));
+    x += s_end - s_begin;
+    const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
+    auto issue = [&](int k) {
+      const int64_t at = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp + k * kWarps) * kStep;
+      const uint32_t st = (it + k) % S;
+      uint8_t* dst = ring + st * R::kStage;
+      uint64_t* bb = bar + st;
+      mbar_arrive_expect_tx(bb, R::kKc + R::kKs + (add ? R::kW : 0));
+      bulk_load(dst, p.c.kc + at * (D / 2), R::kKc, bb);
+      bulk_load(dst + R::kKc, p.c.ks + at * (D / 16), R::kKs, bb);
+      if (add) bulk_load(dst + R::kKc + R::kKs, p.weights + at, R::kW, bb);
+    };
+    if (lane == 0)
+      for (int k = 0; k < min(n_steps, S); ++k) issue(k);
+    for (int i = warp; i < groups * 4; i += kWarps) {
+      uint8_t* grp = smem_q + (i >> 2) * R::kGroupQ;
+      fold_query_fragment<D>(p, b, hk, G, i, rows, i & 3, lane, grp);
+      if (lane == 0) {
+        // a row that saw nothing (lse = -inf) and rows behind the last give no weight
+        float y = -INFINITY;
+        if (i < rows) y = p.w_lse[((int64_t)b * p.heads_q + hk * G + i / p.sq) * p.sq + i % p.sq];
+        reinterpret_cast<float*>(grp + D / 16 * 32 * 8)[i & 3] = y == -INFINITY ? -INFINITY : -y * kLog2e;
       }
     }
-    // Sum over the 8 lanes with the same c, each ending with one token: the
-    // exchange halves the values each lane still carries.
-    float v4[4], v2[2];
-    const bool up16 = lane & 16, up8 = lane & 8, up4 = lane & 4;
+    __syncthreads();
+    uint32_t q[D / 16][2];
+    load_query_fragments<D>(smem_q, lane, q);
+    bool ok = true;
+    for (int k = 0; k < n_steps; ++k) {
+      const uint32_t st = (it + k) % S;
+      ok = warp_wait(bar + st, ((it + k) / S) & 1, p.status, kErrRingW);
+      if (!ok) break;
+      const uint8_t* kc = ring + st * R::kStage;
+      const uint8_t* ks = kc + R::kKc;
+      const int tok = (s_begin + warp + k * kWarps) * kStep;
+      float sum[4];             // tokens g, g + 8, g + 16, g + 24
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = sum[i >> 1][i & 1], e = sum[2 + (i >> 1)][i & 1];
-      const float other = __shfl_xor_sync(0xffffffffu, up16 ? a : e, 16);
-      v4[i] = (up16 ? e : a) + other;
+      for (int u = 0; u < 2; ++u) {
+        uint32_t a[D / 16][4];
+        key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a);
+        float t0 = 0.f, t1 = 0.f;
+        for (int n = 0; n < groups; ++n) {
+          const uint8_t* grp = smem_q + n * R::kGroupQ;
+          if (groups > 1) load_query_fragments<D>(grp, lane, q);
+          const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + (c & 1) * 8);
+          float s[4];
+          score<D>(a, q, s);
+          t0 += fast_exp2(s[0] + neg.x) + fast_exp2(s[1] + neg.y);
+          t1 += fast_exp2(s[2] + neg.x) + fast_exp2(s[3] + neg.y);
+        }
+        sum[2 * u] = t0 + __shfl_xor_sync(0xffffffffu, t0, 1);
+        sum[2 * u + 1] = t1 + __shfl_xor_sync(0xffffffffu, t1, 1);
+      }
+      // every lane of a quad has the four sums: lane c writes token g + 8c
+      const float total = c < 2 ? (c == 0 ? sum[0] : sum[1]) : (c == 2 ? sum[2] : sum[3]);
+      const int at = g + 8 * c;
+      if (tok + at < len) {
+        const float old = add ? reinterpret_cast<const float*>(ks + R::kKs)[at] : 0.f;
+        p.weights[(int64_t)bh * p.c.cap + tok + at] = add ? fmaf(p.decay, old, total) : total;
+      }
+      __syncwarp();
+      if (lane == 0 && k + S < n_steps) issue(k + S);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, up8 ? v4[i] : v4[2 + i], 8);
-      v2[i] = (up8 ? v4[2 + i] : v4[i]) + other;
-    }
-    const float other = __shfl_xor_sync(0xffffffffu, up4 ? v2[0] : v2[1], 4);
-    const float total = (up4 ? v2[1] : v2[0]) + other;
-    const int at = (up16 ? 16 : 0) + (up8 ? 8 : 0) + 2 * c + (up4 ? 1 : 0);
-    if (tok + at < len) {
-      const float old = add ? reinterpret_cast<const float*>(ks + R::kKs)[at] : 0.f;
-      p.weights[(int64_t)bh * p.c.cap + tok + at] = add ? fmaf(p.decay, old, total) : total;
-    }
-    __syncwarp();
-    if (lane == 0 && k + kStages < n_steps) issue(k + kStages);
+    it += n_steps;
+    if (__syncthreads_or(!ok)) return;
   }
 }
 
-template <typename F>
-cudaError_t allow_smem(F* f, int bytes) {
-  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
+int row_tile(int rows) { return rows <= 4 ? 4 : 8; }
 
 }  // namespace
 
-// Parts a history is cut into: enough CTAs for three on each of 148 SMs, of at
-// least 128 tokens (a step of each warp) if the cache is full.
-int token_splits(const Cache& c, int row_tiles) {
-  const int64_t groups = (int64_t)c.batch * c.heads * row_tiles;
-  const int64_t want = std::max<int64_t>(1, 148 * 3 / groups);
-  return (int)std::min<int64_t>({want, (int64_t)(c.cap + kStep * kWarps - 1) / (kStep * kWarps), (int64_t)128});
+// CTAs of the token kernels: as many as run at once (4 an SM, 3 with two row
+// groups), but no more than have a step for each warp if the cache is full.
+int token_ctas(const Cache& c, int rows, bool weights) {
+  const int tile = weights ? rows : row_tile(rows);
+  const int64_t hist = (int64_t)c.batch * c.heads * ((rows + tile - 1) / tile);
+  const int64_t useful = hist * ((c.cap + kStep * kWarps - 1) / (kStep * kWarps));
+  return (int)std::min<int64_t>(useful, 148 * (weights || tile == 4 ? 4 : 3));
 }
 
-template <int D>
+// Rows of pieces: (slots) x (rows of a tile).
+int64_t token_piece_rows(const Cache& c, int rows) {
+  const int tile = row_tile(rows);
+  return ((int64_t)c.batch * c.heads * ((rows + tile - 1) / tile) + token_ctas(c, rows, false)) * tile;
+}
+
+template <int D, int NT>
 static cudaError_t token_fwd_d(const FwdParams4& p, cudaStream_t s) {
-  using R = Ring<D>;
+  using R = Ring<D, NT>;
   const int rows = p.heads_q / p.c.heads * p.sq;
-  const cudaError_t e = allow_smem(kv4_token_fwd_kernel<D>, R::kTotal);
+  static SmemRecord have;
+  cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT>, R::kTotal, have);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.n_splits, (rows + kTokenRows - 1) / kTokenRows, p.c.batch * p.c.heads);
-  kv4_token_fwd_kernel<D><<<grid, kThreads, R::kTotal, s>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s) {
-  return p.c.dim == 128 ? token_fwd_d<128>(p, s) : token_fwd_d<64>(p, s);
-}
-
-cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s) {
-  const int64_t rows = (int64_t)p.c.batch * p.heads_q * p.sq;
+  const int ctas = token_ctas(p.c, rows, false);
+  kv4_token_fwd_kernel<D, NT><<<ctas, kThreads, R::kTotal, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  cfg.gridDim = dim3((unsigned)((int64_t)p.c.batch * p.heads_q * p.sq));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at;
@@ -476,17 +710,23 @@ cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return p.c.dim == 128 ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<128>, p)
-                        : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<64>, p);
+  return cudaLaunchKernelEx(&cfg, kv4_token_combine_kernel<D>, p, 4 * NT, ctas);
+}
+
+cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s) {
+  const bool one = row_tile(p.heads_q / p.c.heads * p.sq) == 4;
+  if (p.c.dim == 128) return one ? token_fwd_d<128, 1>(p, s) : token_fwd_d<128, 2>(p, s);
+  return one ? token_fwd_d<64, 1>(p, s) : token_fwd_d<64, 2>(p, s);
 }
 
 template <int D>
 static cudaError_t token_weights_d(const FwdParams4& p, cudaStream_t s) {
-  const int rows = p.heads_q / p.c.heads * p.sq, tiles = (rows + kTokenRows - 1) / kTokenRows;
-  const int bytes = RingW<D>::bytes(tiles);
-  const cudaError_t e = allow_smem(kv4_token_weights_kernel<D>, bytes);
+  const int rows = p.heads_q / p.c.heads * p.sq, groups = (rows + 3) / 4;
+  const int bytes = RingW<D>::bytes(groups);
+  static SmemRecord have;
+  const cudaError_t e = allow_smem(kv4_token_weights_kernel<D>, bytes, have);
   if (e != cudaSuccess) return e;
-  kv4_token_weights_kernel<D><<<dim3(p.n_splits, p.c.batch * p.c.heads), kThreads, bytes, s>>>(p, tiles);
+  kv4_token_weights_kernel<D><<<token_ctas(p.c, rows, true), kThreads, bytes, s>>>(p, groups);
   return cudaGetLastError();
 }
 

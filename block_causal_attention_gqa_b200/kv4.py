@@ -35,6 +35,8 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.magi_bca_kv4_fwd.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, qp, vp]
     lib.magi_bca_kv4_weights.argtypes = [vp, cp, vp, vp, vp, vp, vp, vp, f32, vp, sz, qp, vp]
     lib.magi_bca_kv4_evict.argtypes = [cp, vp, vp, i32, i32, cp, vp, vp, vp, vp]
+    global _lib
+    _lib = lib
     for name in ("append", "read", "fwd", "weights", "evict"):
         getattr(lib, "magi_bca_kv4_" + name).restype = ctypes.c_int
     for name in ("fwd", "weights"):
@@ -65,67 +67,92 @@ def magi_bca_kv4_cache(batch: int, heads_kv: int, head_dim: int, capacity: int, 
                     z(batch, heads_kv, cap // 2, head_dim), z(batch, heads_kv, cap // 2, head_dim // 16, 2))
 
 
-def _struct(cache, device, name="cache") -> CacheStruct:
+# A decoding step calls these with a few microseconds of device work behind
+# them, so the checks are written for the good case: one expression a tensor,
+# and the reason looked for only where it fails.
+_lib = None
+
+
+def _refuse(name, t, dtype, shape, index):
+    """Says what is wrong with an argument (never returns)."""
+    import torch
+    kind = str(dtype)[6:]
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {kind} CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
+
+
+def _check(name, t, dtype, shape, index):
+    """The tensor's address, if it is a contiguous one of this type and shape on device `index`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, dtype, shape, index)
+
+
+def _struct(cache, index, name="cache") -> CacheStruct:
     """Checks a cache's tensors and fills the C struct."""
     import torch
+    u8 = torch.uint8
     kc, ks, vc, vs = cache
-    for part, t in (("k_codes", kc), ("k_scales", ks), ("v_codes", vc), ("v_scales", vs)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"{name}.{part} must be a contiguous uint8 CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{name}.{part} is on {t.device}, the call runs on {device}")
-    if kc.dim() != 4:
-        raise ValueError(f"{name}.k_codes has shape {tuple(kc.shape)}, expected [batch, heads_kv, capacity, head_dim/2]")
-    B, H, cap, half = kc.shape
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
+        raise TypeError(f"{name}.k_codes must be a uint8 CUDA tensor [batch, heads_kv, capacity, head_dim/2]")
+    shape = kc.shape
+    B, H, cap, half = shape
     D = 2 * half
-    for part, t, shape in (("k_scales", ks, (B, H, cap, D // 16)), ("v_codes", vc, (B, H, cap // 2, D)),
-                           ("v_scales", vs, (B, H, cap // 2, D // 16, 2))):
-        if t.shape != shape:
-            raise ValueError(f"{name}.{part} has shape {tuple(t.shape)}, expected {shape}")
-    return CacheStruct(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), B, H, D, cap)
+    return CacheStruct(_check(name + ".k_codes", kc, u8, shape, index),
+                       _check(name + ".k_scales", ks, u8, (B, H, cap, D // 16), index),
+                       _check(name + ".v_codes", vc, u8, (B, H, cap // 2, D), index),
+                       _check(name + ".v_scales", vs, u8, (B, H, cap // 2, D // 16, 2), index), B, H, D, cap)
 
 
-def _check(name, t, dtype, shape, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    return t.data_ptr()
-
-
-def _check_rope(name, t, batch, n, half, device):
+def _check_rope(name, t, batch, n, half, index):
     """(pointer, batch stride in elements) of an angle table [n, D/2] or [B, n, D/2]."""
     import torch
     if t is None:
         return None, 0
     if isinstance(t, torch.Tensor) and t.dim() == 3:
-        return _check(name, t, torch.float32, (batch, n, half), device), n * half
-    return _check(name, t, torch.float32, (n, half), device), 0
+        return _check(name, t, torch.float32, (batch, n, half), index), n * half
+    return _check(name, t, torch.float32, (n, half), index), 0
 
 
-def _device_of(name, t, dims=4):
+def _device_of(name, t):
+    """The device index a call runs on: that of its first tensor."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
-    return t.device
+    if t.dim() != 4:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected 4 dimensions")
+    return t.get_device()
 
 
-def _call(name, device, stream, *args):
-    """Runs an entry point on `device`; the stream goes last."""
+def _library():
+    """The loaded library (declare() has set it)."""
+    if _lib is None:
+        from . import library
+        return library()
+    return _lib
+
+
+def _call(name, index, stream, *args):
+    """Runs an entry point on device `index`; the stream goes last."""
     import torch
-    from . import MagiBcaError, _stream_handle, library
-    f = getattr(library(), name)
-    if torch.cuda.current_device() == device.index:
-        st = f(*args, _stream_handle(stream, device))
+    f = getattr(_library(), name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(device):
-            st = f(*args, _stream_handle(stream, device))
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        st = f(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, handle)
     if st != 0:
+        from . import MagiBcaError
         raise MagiBcaError(st, name)
 
 
@@ -136,14 +163,15 @@ def magi_bca_kv4_append(cache, k, v, start, counts=None, rope_k=None, rms_eps: f
     [B, n, D/2] applied to k before its norm."""
     import torch
     dev = _device_of("k", k)
-    B, n, H, D = k.shape
+    shape = k.shape
+    B, n, H, D = shape
     c = _struct(cache, dev)
     if (c.batch, c.heads_kv, c.head_dim) != (B, H, D):
         raise ValueError(f"k has shape {tuple(k.shape)}, the cache holds batch {c.batch}, {c.heads_kv} heads of {c.head_dim}")
     if n < 1:
         return
-    kp = _check("k", k, torch.bfloat16, k.shape, dev)
-    vp = _check("v", v, torch.bfloat16, k.shape, dev)
+    kp = _check("k", k, torch.bfloat16, shape, dev)
+    vp = _check("v", v, torch.bfloat16, shape, dev)
     sp = _check("start", start, torch.int32, (B,), dev)
     np_ = _check("counts", counts, torch.int32, (B,), dev) if counts is not None else None
     rp, rs = _check_rope("rope_k", rope_k, B, n, D // 2, dev)
@@ -156,42 +184,47 @@ def magi_bca_kv4_read(cache, start, n: int, k=None, v=None, stream=None):
     import torch
     dev = _device_of("cache.k_codes", cache[0])
     c = _struct(cache, dev)
-    shape = (c.batch, int(n), c.heads_kv, c.head_dim)
-    k = torch.empty(shape, device=dev, dtype=torch.bfloat16) if k is None else k
-    v = torch.empty(shape, device=dev, dtype=torch.bfloat16) if v is None else v
+    n = int(n)
+    shape = (c.batch, n, c.heads_kv, c.head_dim)
+    k = cache[0].new_empty(shape, dtype=torch.bfloat16) if k is None else k
+    v = cache[0].new_empty(shape, dtype=torch.bfloat16) if v is None else v
     kp = _check("k", k, torch.bfloat16, shape, dev)
     vp = _check("v", v, torch.bfloat16, shape, dev)
     sp = _check("start", start, torch.int32, (c.batch,), dev) if start is not None else None
     if n > 0:
-        _call("magi_bca_kv4_read", dev, stream, ctypes.byref(c), sp, int(n), kp, vp)
+        _call("magi_bca_kv4_read", dev, stream, ctypes.byref(c), sp, n, kp, vp)
     return k, v
 
 
 def _query(q, c, gamma_q, gamma_k, rope_q, softmax_scale, rms_eps, dev):
     """Checks the query side; returns (q, gamma_q, gamma_k, angles) pointers and the C struct."""
     import torch
-    B, Sq, Hq, D = q.shape
-    if (c.batch, c.head_dim) != (B, D):
-        raise ValueError(f"q has shape {tuple(q.shape)}, the cache holds batch {c.batch}, heads of {c.head_dim}")
+    shape = q.shape
+    B, Sq, Hq, D = shape
+    if c.batch != B or c.head_dim != D:
+        raise ValueError(f"q has shape {tuple(shape)}, the cache holds batch {c.batch}, heads of {c.head_dim}")
+    if Sq < 1:
+        raise ValueError("q has no tokens")
+    f32 = torch.float32
     rp, rs = _check_rope("rope_q", rope_q, B, Sq, D // 2, dev)
-    ptrs = (_check("q", q, torch.bfloat16, q.shape, dev), _check("gamma_q", gamma_q, torch.float32, (D,), dev),
-            _check("gamma_k", gamma_k, torch.float32, (D,), dev), rp)
-    return ptrs, QueryStruct(Sq, Hq, float(softmax_scale), float(rms_eps), rs)
+    return ((_check("q", q, torch.bfloat16, shape, dev), _check("gamma_q", gamma_q, f32, (D,), dev),
+             _check("gamma_k", gamma_k, f32, (D,), dev), rp),
+            QueryStruct(Sq, Hq, softmax_scale, rms_eps, rs))
 
 
-def _workspace(size_fn, c, query, workspace, dev):
+def _workspace(size_fn, c, query, workspace, q):
     """(pointer, bytes, tensor) of the caller's workspace or a new one."""
     import torch
-    from . import library
     if workspace is None:
-        n = getattr(library(), size_fn)(ctypes.byref(c), ctypes.byref(query))
+        n = getattr(_library(), size_fn)(ctypes.byref(c), ctypes.byref(query))
         if n == 0:
             return None, 0, None
-        workspace = torch.empty(n, device=dev, dtype=torch.uint8)
-    elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        workspace = q.new_empty(n, dtype=torch.uint8)
+        return workspace.data_ptr(), n, workspace
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the call runs on {dev}")
+    if workspace.device != q.device:
+        raise ValueError(f"workspace is on {workspace.device}, the call runs on {q.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -214,20 +247,21 @@ def magi_bca_kv4_fwd(q, cache, lengths, gamma_q, gamma_k, rope_q=None, base_out=
     dev = _device_of("q", q)
     c = _struct(cache, dev)
     (qp, gq, gk, rp), query = _query(q, c, gamma_q, gamma_k, rope_q, softmax_scale, rms_eps, dev)
-    B, Sq, Hq, D = q.shape
+    shape, bf16, f32 = q.shape, torch.bfloat16, torch.float32
+    rows = (shape[0], shape[2], shape[1])
     if (base_out is None) != (base_lse is None):
         raise ValueError("base_out and base_lse go together")
-    if Sq < 1:
-        raise ValueError("q has no tokens")
     out = torch.empty_like(q) if out is None else out
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, Sq, device=dev, dtype=torch.float32)
-    op = _check("out", out, torch.bfloat16, q.shape, dev)
-    lp = _check("lse", lse, torch.float32, (B, Hq, Sq), dev) if lse is not None else None
-    bo = _check("base_out", base_out, torch.bfloat16, q.shape, dev) if base_out is not None else None
-    bl = _check("base_lse", base_lse, torch.float32, (B, Hq, Sq), dev) if base_lse is not None else None
-    ln = _check("lengths", lengths, torch.int32, (B,), dev)
-    wp, wb, ws = _workspace("magi_bca_kv4_fwd_workspace_size", c, query, workspace, dev)
+        lse = q.new_empty(rows, dtype=f32)
+    op = _check("out", out, bf16, shape, dev)
+    lp = _check("lse", lse, f32, rows, dev) if lse is not None else None
+    bo = bl = None
+    if base_out is not None:
+        bo = _check("base_out", base_out, bf16, shape, dev)
+        bl = _check("base_lse", base_lse, f32, rows, dev)
+    ln = _check("lengths", lengths, torch.int32, rows[:1], dev)
+    wp, wb, ws = _workspace("magi_bca_kv4_fwd_workspace_size", c, query, workspace, q)
     _call("magi_bca_kv4_fwd", dev, stream, qp, ctypes.byref(c), ln, gq, gk, rp, bo, bl, op, lp, wp, wb,
           ctypes.byref(query))
     if workspace is None:
@@ -244,13 +278,11 @@ def magi_bca_kv4_weights(q, cache, lengths, lse, gamma_q, gamma_k, weights, rope
     dev = _device_of("q", q)
     c = _struct(cache, dev)
     (qp, gq, gk, rp), query = _query(q, c, gamma_q, gamma_k, rope_q, softmax_scale, rms_eps, dev)
-    B, Sq, Hq, D = q.shape
-    if Sq < 1:
-        raise ValueError("q has no tokens")
+    B, Sq, Hq, _ = q.shape
     lp = _check("lse", lse, torch.float32, (B, Hq, Sq), dev)
     w = _check("weights", weights, torch.float32, (c.batch, c.heads_kv, c.capacity), dev)
     ln = _check("lengths", lengths, torch.int32, (B,), dev)
-    wp, wb, ws = _workspace("magi_bca_kv4_weights_workspace_size", c, query, workspace, dev)
+    wp, wb, ws = _workspace("magi_bca_kv4_weights_workspace_size", c, query, workspace, q)
     _call("magi_bca_kv4_weights", dev, stream, qp, ctypes.byref(c), ln, lp, gq, gk, rp, w, float(decay), wp, wb,
           ctypes.byref(query))
     if workspace is None:
@@ -277,8 +309,8 @@ def magi_bca_kv4_evict(cache, weights, lengths, keep: int, recent: int, dst_cach
     w = _check("weights", weights, torch.float32, (B, H, c.capacity), dev)
     dw = _check("dst_weights", dst_weights, torch.float32, (B, H, d.capacity), dev)
     ln = _check("lengths", lengths, torch.int32, (B,), dev)
-    dst_lengths = torch.empty(B, device=dev, dtype=torch.int32) if dst_lengths is None else dst_lengths
-    index = torch.empty(B, H, keep, device=dev, dtype=torch.int32) if index is None else index
+    dst_lengths = lengths.new_empty(B) if dst_lengths is None else dst_lengths
+    index = lengths.new_empty((B, H, keep)) if index is None else index
     dl = _check("dst_lengths", dst_lengths, torch.int32, (B,), dev)
     ix = _check("index", index, torch.int32, (B, H, keep), dev)
     _call("magi_bca_kv4_evict", dev, stream, ctypes.byref(c), w, ln, keep, recent, ctypes.byref(d), dw, dl, ix)
@@ -286,9 +318,8 @@ def magi_bca_kv4_evict(cache, weights, lengths, keep: int, recent: int, dst_cach
 
 
 def _size(size_fn, cache, seqlen_q, heads_q):
-    from . import library
-    c = _struct(cache, cache[0].device)
-    return int(getattr(library(), size_fn)(ctypes.byref(c), ctypes.byref(QueryStruct(seqlen_q, heads_q, 0.0, 0.0, 0))))
+    c = _struct(cache, _device_of("cache.k_codes", cache[0]))
+    return int(getattr(_library(), size_fn)(ctypes.byref(c), ctypes.byref(QueryStruct(seqlen_q, heads_q, 0.0, 0.0, 0))))
 
 
 def magi_bca_kv4_fwd_workspace_size(cache, seqlen_q: int, heads_q: int) -> int:

@@ -159,8 +159,8 @@ def test_evict_arguments():
 def test_workspace_sizes():
     lib = bca.library()
     c = ctypes.byref(cache(batch=1, heads_kv=64, capacity=128))
-    # 64 heads of one part each: no parts to join, nothing to expand
-    assert lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(heads_q=64))) == 0
+    # a single token: pieces of rows to join, far less than the cache; its weights need nothing
+    assert 0 < lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(heads_q=64))) < 1 << 20
     assert lib.magi_bca_kv4_weights_workspace_size(c, ctypes.byref(query(heads_q=64))) == 0
     # a chunk: the expanded cache and queries at least
     c = ctypes.byref(cache(batch=2, heads_kv=8, capacity=92160))
