@@ -51,10 +51,10 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 // One scale byte in both halves of an fp16 pair.
-__device__ __forceinline__ uint32_t scale_dup(uint32_t byte) { return (byte << 7) * 0x10001u; }
+__device__ __forceinline__ uint32_t scale_dup(uint32_t byte) { return byte * (0x10001u << 7); }
 
-// Two scale bytes (b0 in the low half) as an fp16 pair.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t b0, uint32_t b1) { return (b0 << 7) | (b1 << 23); }
+// The two scale bytes of a 16-bit word (low byte in the low half) as an fp16 pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t b2) { return __byte_perm(b2, 0, 0x4140) << 7; }
 
 // fp16 pair -> bf16 pair; exact for cached values.
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {

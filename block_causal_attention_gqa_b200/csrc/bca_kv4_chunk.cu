@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(256) kv4_expand_kernel(const FwdParams4 p, int
         const int64_t vrow = tok0 / 2 + pr;
         const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.c.vc + vrow * D + f));
         const uint32_t s2 = __ldg(reinterpret_cast<const uint16_t*>(p.c.vs + (vrow * (D / 16) + f / 16) * 2));
-        uint32_t s = scale_pair(s2 & 0xffu, s2 >> 8);
+        uint32_t s = scale_pair(s2);
         const int t = tile * 128 + 2 * pr;
         if (t + 1 >= len) s = t >= len ? 0u : s & 0xffffu;
         uint32_t a[8];

@@ -12,11 +12,14 @@
 // operands, and all the work per value left to the CUDA cores is half a
 // conversion (e2m1x2 -> f16x2) and half a multiplication by the block's scale.
 //   - Keys and values are the A operand (M = 16 tokens, or 16 features), the
-//     rows of the queries are N.  The cached values are exact in fp16; the
-//     other operand is split in two fp16 numbers, x = hi + lo, so that scores
-//     and sums are good to fp32's last bits: 4 rows fill N = 0..3 with hi and
-//     N = 4..7 with lo.  (With the rows as M the same products took twice the
-//     matrix instructions and twice the accumulators.)
+//     rows of the queries are N.  The cached values are exact in fp16; a query
+//     is split in two fp16 numbers, q = hi + lo, so that scores are good to
+//     fp32's last bits: 4 rows fill N = 0..3 with hi and N = 4..7 with lo.  P
+//     is one fp16 number (half a step is 2^-11, against 2^-8 of the bf16
+//     result, and its sum is taken in fp32 before it is rounded), so 8 rows fill
+//     the second product.  (With the rows as M the same products took twice
+//     the matrix instructions and twice the accumulators: 102 us against 78 at
+//     4 x 92160 tokens of 8 heads, one query each.)
 //   - The layouts of the fragments are met by renaming, not by moving data.
 //     The features of a dot product may be summed in any order, so lane c of a
 //     quad holds a contiguous quarter of a key row; and the features of the
@@ -28,8 +31,8 @@
 //   - P is scaled by 2^7 (reference m - 7) and m moves only when a score passes
 //     it by 8, so P stays below 2^15 in fp16 and loses nothing above 2^-31.
 //   - Each warp streams its own steps of 32 tokens through its own ring of
-//     bulk copies (one lane issues, mbarriers complete), so warps do not wait
-//     for one another until the end.
+//     bulk copies (a lane for each of the four arrays, mbarriers complete), so
+//     warps do not wait for one another until the end.
 //
 // Split.  The steps of all histories (batch element, head, row tile) are laid
 // end to end and cut into equal parts, one for each CTA of the grid, so
@@ -61,7 +64,7 @@ enum : int { kErrRing = 3101, kErrRingW = 3102 };
 template <int D, int NT>
 struct Ring {
   static constexpr int kRows = 4 * NT;
-  static constexpr int kKc = kStep * D / 2, kKs = kStep * D / 16, kVc = kStep / 2 * D, kVs = kStep * D / 16;
+  static constexpr int kKc = kStep * D / 2, kKs = kStep * D / 16, kVc = kKc, kVs = kKs;   // a stage: kc, vc, ks, vs
   static constexpr int kStage = kKc + kKs + kVc + kVs;
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kQ = NT * (D / 16) * 32 * 8;       // query fragments of a row tile
@@ -72,8 +75,7 @@ struct Ring {
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -120,16 +122,23 @@ __device__ __forceinline__ void key_fragments(const uint8_t* kc, const uint8_t* 
   }
 }
 
-// Scores of 16 tokens against 4 rows, q the group's B fragments: x[0], x[1]
-// token g, x[2], x[3] token g + 8, rows 2(c & 1) and 2(c & 1) + 1 (lanes c and
-// c ^ 2 hold the same).
+// Products of 16 tokens with 4 rows, q the group's B fragments: acc[0], acc[1]
+// token g, acc[2], acc[3] token g + 8; lanes c < 2 the hi parts of rows 2c and
+// 2c + 1, lanes c >= 2 the lo parts of rows 2(c - 2) and 2(c - 2) + 1.  Two
+// accumulators, for two shorter chains.
 template <int D>
-__device__ __forceinline__ void score(const uint32_t (&a)[D / 16][4], const uint32_t (&q)[D / 16][2], float (&x)[4]) {
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void products(const uint32_t (&a)[D / 16][4], const uint32_t (&q)[D / 16][2],
+                                         float (&acc)[4]) {
+  float odd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) mma16816(acc, a[j], q[j][0], q[j][1]);
+  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = acc[i] + __shfl_xor_sync(0xffffffffu, acc[i], 2);   // hi + lo
+  for (int j = 0; j < D / 16; j += 2) {
+    mma16816(acc, a[j], q[j][0], q[j][1]);
+    mma16816(odd, a[j + 1], q[j + 1][0], q[j + 1][1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] += odd[i];
 }
 
 template <int D>
@@ -242,6 +251,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
   int64_t begin = where[2];     // flat step where batch element b begins
   int b = (int)where[3];
   uint32_t it = 0;              // steps this warp has begun, over all pieces
+  const uint32_t bytes = lane < 2 ? R::kKc : R::kKs;     // of the array this lane copies, and its place in a stage
+  const uint32_t to = lane == 0 ? 0 : lane == 1 ? R::kKc : lane == 2 ? 2 * R::kKc : 2 * R::kKc + R::kKs;
 
   while (x < x1) {              // one piece: steps [s_begin, s_end) of one history
     const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
@@ -260,19 +271,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     x += s_end - s_begin;
 
     const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
-    auto issue = [&](int k) {   // by lane 0
-      const int64_t at = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp + k * kWarps) * kStep;
+    // lanes 0..3 each copy from one of the four arrays
+    const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
+    const uint8_t* from = lane == 0   ? p.c.kc + at0 * (D / 2)
+                          : lane == 1 ? p.c.vc + at0 / 2 * D
+                          : lane == 2 ? p.c.ks + at0 * (D / 16)
+                                      : p.c.vs + at0 * (D / 16);
+    auto issue = [&](int k) {
       const uint32_t st = (it + k) % kStages;
-      uint8_t* dst = ring + st * R::kStage;
-      uint64_t* bb = bar + st;
-      mbar_arrive_expect_tx(bb, R::kStage);
-      bulk_load(dst, p.c.kc + at * (D / 2), R::kKc, bb);
-      bulk_load(dst + R::kKc, p.c.ks + at * (D / 16), R::kKs, bb);
-      bulk_load(dst + R::kKc + R::kKs, p.c.vc + at / 2 * D, R::kVc, bb);
-      bulk_load(dst + R::kKc + R::kKs + R::kVc, p.c.vs + at * (D / 16), R::kVs, bb);
+      if (lane == 0) mbar_arrive_expect_tx(bar + st, R::kStage);
+      __syncwarp();
+      if (lane < 4) bulk_load(ring + st * R::kStage + to, from + (int64_t)k * kWarps * bytes, bytes, bar + st);
     };
-    if (lane == 0)
-      for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
+    for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
 
     // the row tile's queries, while the first copies are under way
     for (int i = warp; i < kRows; i += kWarps)
@@ -282,77 +293,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
 #pragma unroll
     for (int t = 0; t < NT; ++t) load_query_fragments<D>(smem_q + t * (D / 16) * 32 * 8, lane, q[t]);
 
-    float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
+    // this lane's two rows of the tile: r0 and r0 + 1 (NT = 1: lanes c and c ^ 2 hold the same)
+    float o[D / 16][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = -INFINITY;
-      l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
-    }
+    for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     bool ok = true;
     for (int k = 0; k < n_steps; ++k) {
       const uint32_t st = (it + k) % kStages;
       ok = warp_wait(bar + st, ((it + k) / kStages) & 1, p.status, kErrRing);
       if (!ok) break;
       const uint8_t* kc = ring + st * R::kStage;
-      const uint8_t* ks = kc + R::kKc;
-      const uint8_t* vc = ks + R::kKs;
-      const uint8_t* vs = vc + R::kVc;
+      const uint8_t* vc = kc + R::kKc;
+      const uint8_t* ks = vc + R::kVc;
+      const uint8_t* vs = ks + R::kKs;
       const int tok = (s_begin + warp + k * kWarps) * kStep;
       const bool tail = tok + kStep > len;
-      float s[NT][2][4];
+      float s[2][4];             // [16 tokens][token g: row r0, r0 + 1; token g + 8: the same]
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t a[D / 16][4];
         key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a);
+        float acc[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          score<D>(a, q[t], s[t][u]);
-          if (tail) {
-            if (tok + u * 16 + g >= len) s[t][u][0] = s[t][u][1] = -INFINITY;
-            if (tok + u * 16 + g + 8 >= len) s[t][u][2] = s[t][u][3] = -INFINITY;
+        for (int t = 0; t < NT; ++t) products<D>(a, q[t], acc[t]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // hi + lo, of the lane's own group
+          if constexpr (NT == 1) {
+            s[u][i] = acc[0][i] + __shfl_xor_sync(0xffffffffu, acc[0][i], 2);
+          } else {
+            const float other = __shfl_xor_sync(0xffffffffu, c < 2 ? acc[1][i] : acc[0][i], 2);
+            s[u][i] = (c < 2 ? acc[0][i] : acc[1][i]) + other;
           }
         }
       }
-      uint32_t pb[NT][2][2];   // P as B fragments: [group][16 tokens][8 tokens]
+      if (tail) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float top[2];
+        for (int u = 0; u < 2; ++u) {
+          if (tok + u * 16 + g >= len) s[u][0] = s[u][1] = -INFINITY;
+          if (tok + u * 16 + g + 8 >= len) s[u][2] = s[u][3] = -INFINITY;
+        }
+      }
+      float top[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmax3(s[t][0][r], s[t][0][r + 2], s[t][1][r]), s[t][1][r + 2]);
-        if (__any_sync(0xffffffffu, top[0] > m[t][0] + kMove || top[1] > m[t][1] + kMove)) {
+      for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmax3(s[0][r], s[0][r + 2], s[1][r]), s[1][r + 2]);
+      if (__any_sync(0xffffffffu, top[0] > m[0] + kMove || top[1] > m[1] + kMove)) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
-            for (int i = 4; i < 32; i <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], i));
-            const float m1 = fmaxf(m[t][r], top[r]);
-            const float alpha = m1 == -INFINITY ? 1.f : fast_exp2(m[t][r] - m1);
-            m[t][r] = m1;
-            l[t][r] *= alpha;
+          for (int i = 4; i < 32; i <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], i));
+          const float m1 = fmaxf(m[r], top[r]);
+          const float alpha = m1 == -INFINITY ? 1.f : fast_exp2(m[r] - m1);
+          m[r] = m1;
+          l[r] *= alpha;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              o[t][j][r] *= alpha;
-              o[t][j][r + 2] *= alpha;
-            }
+          for (int j = 0; j < D / 16; ++j) {
+            o[j][r] *= alpha;
+            o[j][r + 2] *= alpha;
           }
         }
-        const float shift0 = m[t][0] == -INFINITY ? 0.f : kLift - m[t][0];
-        const float shift1 = m[t][1] == -INFINITY ? 0.f : kLift - m[t][1];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p0 = fast_exp2(s[t][u][2 * h] + shift0), p1 = fast_exp2(s[t][u][2 * h + 1] + shift1);
-            l[t][0] += p0;
-            l[t][1] += p1;
-            const uint32_t hi = pack_f16x2(p0, p1);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-            const uint32_t lo = pack_f16x2(p0 - back.x, p1 - back.y);
-            pb[t][u][h] = transpose8(c < 2 ? hi : lo);
-          }
       }
+      const float shift0 = m[0] == -INFINITY ? 0.f : kLift - m[0];
+      const float shift1 = m[1] == -INFINITY ? 0.f : kLift - m[1];
+      uint32_t pb[2][2];   // P as B fragments: [16 tokens][8 tokens]
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = fast_exp2(s[u][2 * h] + shift0), p1 = fast_exp2(s[u][2 * h + 1] + shift1);
+          l[0] += p0;
+          l[1] += p1;
+          pb[u][h] = transpose8(pack_f16x2(p0, p1));
+        }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t v[2][D / 32], sc[2];
@@ -368,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
             v[i][0] = w.x; v[i][1] = w.y;
           }
           const uint32_t s2 = *reinterpret_cast<const uint16_t*>(vs + (row * (D / 16) + g * (D / 8) / 16) * 2);
-          sc[i] = scale_pair(s2 & 0xffu, s2 >> 8);
+          sc[i] = scale_pair(s2);
           if (tail) {   // rows behind the end may hold anything: their values count as zero
             if (tok + 2 * row >= len) sc[i] = 0u;
             else if (tok + 2 * row + 1 >= len) sc[i] &= 0xffffu;
@@ -384,13 +396,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
           for (int j = 0; j < 2; ++j) {
             const uint32_t a[4] = {hmul2(h0[2 * j], sc[0]), hmul2(h0[2 * j + 1], sc[0]), hmul2(h1[2 * j], sc[1]),
                                    hmul2(h1[2 * j + 1], sc[1])};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(o[t][2 * i + j], a, pb[t][u][0], pb[t][u][1]);
+            mma16816(o[2 * i + j], a, pb[u][0], pb[u][1]);
           }
         }
       }
       __syncwarp();
-      if (lane == 0 && k + kStages < n_steps) issue(k + kStages);
+      if (k + kStages < n_steps) issue(k + kStages);
     }
     it += n_steps;
     // every issued copy has been waited for; a wait that failed ends the CTA
@@ -398,29 +409,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
 
     // join the warps
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int i = 4; i < 32; i <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], i);
+      // scores that are NaN (a query that is) leave the reference at -inf: they must not pass for an empty row
+      if (m[r] == -INFINITY && !(l[r] == 0.f)) m[r] = kLift;
+      const int row = (NT == 2 ? 4 * (c >> 1) : 0) + 2 * (c & 1) + r;
+      if (NT == 2 || c < 2) {
+        float* dst = smem_merge + (warp * kRows + row) * R::kMergeRow + g * (D / 8);
 #pragma unroll
-        for (int i = 4; i < 32; i <<= 1) l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], i);
-        // scores that are NaN (a query that is) leave the reference at -inf: they must not pass for an empty row
-        if (m[t][r] == -INFINITY && !(l[t][r] == 0.f)) m[t][r] = kLift;
+        for (int j = 0; j < D / 16; j += 2)   // features 2j .. 2j + 3 of the lane group's eighth
+          *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[j][r], o[j][r + 2], o[j + 1][r], o[j + 1][r + 2]);
+        if (g == 0) smem_ml[warp * kRows + row] = make_float2(m[r] - kLift, l[r]);
       }
-      // hi + lo; lanes c < 2 then write row 2c, the others row 2(c - 2) + 1
-      const int own = c >> 1, row = 4 * t + 2 * (c & 1) + own;
-      float* dst = smem_merge + (warp * kRows + row) * R::kMergeRow + g * (D / 8);
-#pragma unroll
-      for (int j = 0; j < D / 16; j += 2) {
-        float f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {   // features 2j .. 2j + 3 of the lane group's eighth
-          const float a0 = o[t][j + (e >> 1)][2 * (e & 1)], a1 = o[t][j + (e >> 1)][2 * (e & 1) + 1];
-          const float b0 = a0 + __shfl_xor_sync(0xffffffffu, a0, 2), b1 = a1 + __shfl_xor_sync(0xffffffffu, a1, 2);
-          f[e] = own ? b1 : b0;
-        }
-        *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(f[0], f[1], f[2], f[3]);
-      }
-      if (g == 0) smem_ml[warp * kRows + row] = make_float2((own ? m[t][1] : m[t][0]) - kLift, own ? l[t][1] : l[t][0]);
     }
     __syncthreads();
 
@@ -591,6 +592,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
   int b = (int)where[3];
   uint32_t it = 0;
   const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
+  const uint32_t bytes = lane == 0 ? R::kKc : lane == 1 ? R::kKs : R::kW;
+  const uint32_t to = lane == 0 ? 0 : lane == 1 ? R::kKc : R::kKc + R::kKs;
 
   while (x < x1) {
     const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
@@ -605,18 +608,18 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
     const int s_end = (int)min((int64_t)steps, s_begin + (x1 - x));
     x += s_end - s_begin;
     const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
+    // lanes 0..2 each copy from one of the arrays
+    const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
+    const uint8_t* from = lane == 0   ? p.c.kc + at0 * (D / 2)
+                          : lane == 1 ? p.c.ks + at0 * (D / 16)
+                                      : reinterpret_cast<const uint8_t*>(p.weights + at0);
     auto issue = [&](int k) {
-      const int64_t at = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp + k * kWarps) * kStep;
       const uint32_t st = (it + k) % S;
-      uint8_t* dst = ring + st * R::kStage;
-      uint64_t* bb = bar + st;
-      mbar_arrive_expect_tx(bb, R::kKc + R::kKs + (add ? R::kW : 0));
-      bulk_load(dst, p.c.kc + at * (D / 2), R::kKc, bb);
-      bulk_load(dst + R::kKc, p.c.ks + at * (D / 16), R::kKs, bb);
-      if (add) bulk_load(dst + R::kKc + R::kKs, p.weights + at, R::kW, bb);
+      if (lane == 0) mbar_arrive_expect_tx(bar + st, R::kKc + R::kKs + (add ? R::kW : 0));
+      __syncwarp();
+      if (lane < (add ? 3 : 2)) bulk_load(ring + st * R::kStage + to, from + (int64_t)k * kWarps * bytes, bytes, bar + st);
     };
-    if (lane == 0)
-      for (int k = 0; k < min(n_steps, S); ++k) issue(k);
+    for (int k = 0; k < min(n_steps, S); ++k) issue(k);
     for (int i = warp; i < groups * 4; i += kWarps) {
       uint8_t* grp = smem_q + (i >> 2) * R::kGroupQ;
       fold_query_fragment<D>(p, b, hk, G, i, rows, i & 3, lane, grp);
@@ -649,7 +652,9 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
           if (groups > 1) load_query_fragments<D>(grp, lane, q);
           const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + (c & 1) * 8);
           float s[4];
-          score<D>(a, q, s);
+          products<D>(a, q, s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);   // hi + lo
           t0 += fast_exp2(s[0] + neg.x) + fast_exp2(s[1] + neg.y);
           t1 += fast_exp2(s[2] + neg.x) + fast_exp2(s[3] + neg.y);
         }
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
         p.weights[(int64_t)bh * p.c.cap + tok + at] = add ? fmaf(p.decay, old, total) : total;
       }
       __syncwarp();
-      if (lane == 0 && k + S < n_steps) issue(k + S);
+      if (k + S < n_steps) issue(k + S);
     }
     it += n_steps;
     if (__syncthreads_or(!ok)) return;
