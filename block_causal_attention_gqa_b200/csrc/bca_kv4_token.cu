@@ -31,7 +31,7 @@
 //   - P is scaled by 2^7 (reference m - 7) and m moves only when a score passes
 //     it by 8, so P stays below 2^15 in fp16 and loses nothing above 2^-31.
 //   - Each warp streams its own steps of 32 tokens through its own ring of
-//     bulk copies (a lane for each of the four arrays, mbarriers complete), so
+//     bulk copies (one lane issues, mbarriers complete), so
 //     warps do not wait for one another until the end.
 //
 // Split.  The steps of all histories (batch element, head, row tile) are laid
@@ -71,13 +71,18 @@ struct Ring {
   static constexpr int kMergeRow = D + 4;                 // floats, padded
   static constexpr int kMerge = kWarps * kRows * kMergeRow * 4;
   static constexpr int kRing = kWarps * kWarp;
-  static constexpr int kTotal = kRing + kMerge + kQ + kWarps * kRows * 8 + kWarps * kStages * 8 + 32;
+  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;   // the merge reuses the ring
+  static constexpr int kTotal = kBody + kQ + kWarps * kRows * 8 + kWarps * kStages * 8 + 32;
 };
 
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                         float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  mma16816(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 // 8x8 fp16 transpose over the warp.
@@ -89,8 +94,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 // Bounded wait whose outcome the whole warp agrees on.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int code) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
 }
+
+// The warp's number, in a form the compiler knows to be the same for all its
+// lanes: what is computed from it (the addresses of the copies) then lives in
+// uniform registers.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
 
 // A fragments of 16 tokens' keys (rows g and g + 8 of the tile; lane c's
 // quarter of the features): k-step j covers features c D/4 + 4j .. + 3.
@@ -122,23 +133,16 @@ __device__ __forceinline__ void key_fragments(const uint8_t* kc, const uint8_t* 
   }
 }
 
-// Products of 16 tokens with 4 rows, q the group's B fragments: acc[0], acc[1]
-// token g, acc[2], acc[3] token g + 8; lanes c < 2 the hi parts of rows 2c and
-// 2c + 1, lanes c >= 2 the lo parts of rows 2(c - 2) and 2(c - 2) + 1.  Two
-// accumulators, for two shorter chains.
+// Products of 16 tokens with 4 rows, q the group's B fragments, on top of the
+// start values c0 (even row) and c1 (odd row): acc[0], acc[1] token g, acc[2],
+// acc[3] token g + 8; lanes c < 2 the hi parts of rows 2c and 2c + 1, lanes
+// c >= 2 the lo parts of rows 2(c - 2) and 2(c - 2) + 1.
 template <int D>
-__device__ __forceinline__ void products(const uint32_t (&a)[D / 16][4], const uint32_t (&q)[D / 16][2],
-                                         float (&acc)[4]) {
-  float odd[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void products(const uint32_t (&a)[D / 16][4], const uint32_t (&q)[D / 16][2], float c0,
+                                         float c1, float (&acc)[4]) {
+  mma16816(acc, a[0], q[0][0], q[0][1], c0, c1, c0, c1);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
-#pragma unroll
-  for (int j = 0; j < D / 16; j += 2) {
-    mma16816(acc, a[j], q[j][0], q[j][1]);
-    mma16816(odd, a[j + 1], q[j + 1][0], q[j + 1][1]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] += odd[i];
+  for (int j = 1; j < D / 16; ++j) mma16816(acc, a[j], q[j][0], q[j][1]);
 }
 
 template <int D>
@@ -213,12 +217,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
   using R = Ring<D, NT>;
   constexpr int kRows = R::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* smem_merge = reinterpret_cast<float*>(smem + R::kRing);
-  uint8_t* smem_q = smem + R::kRing + R::kMerge;
+  float* smem_merge = reinterpret_cast<float*>(smem);
+  uint8_t* smem_q = smem + R::kBody;
   float2* smem_ml = reinterpret_cast<float2*>(smem_q + R::kQ);            // [warp][row]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_ml + kWarps * kRows); // [warp][stage]
   int64_t* where = reinterpret_cast<int64_t*>(bars + kWarps * kStages);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
   const int row_tiles = (rows + kRows - 1) / kRows;
@@ -251,8 +255,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
   int64_t begin = where[2];     // flat step where batch element b begins
   int b = (int)where[3];
   uint32_t it = 0;              // steps this warp has begun, over all pieces
-  const uint32_t bytes = lane < 2 ? R::kKc : R::kKs;     // of the array this lane copies, and its place in a stage
-  const uint32_t to = lane == 0 ? 0 : lane == 1 ? R::kKc : lane == 2 ? 2 * R::kKc : 2 * R::kKc + R::kKs;
 
   while (x < x1) {              // one piece: steps [s_begin, s_end) of one history
     const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
@@ -271,17 +273,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     x += s_end - s_begin;
 
     const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
-    // lanes 0..3 each copy from one of the four arrays
     const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
-    const uint8_t* from = lane == 0   ? p.c.kc + at0 * (D / 2)
-                          : lane == 1 ? p.c.vc + at0 / 2 * D
-                          : lane == 2 ? p.c.ks + at0 * (D / 16)
-                                      : p.c.vs + at0 * (D / 16);
+    const uint8_t *src_kc = p.c.kc + at0 * (D / 2), *src_vc = p.c.vc + at0 / 2 * D;
+    const uint8_t *src_ks = p.c.ks + at0 * (D / 16), *src_vs = p.c.vs + at0 * (D / 16);
     auto issue = [&](int k) {
-      const uint32_t st = (it + k) % kStages;
-      if (lane == 0) mbar_arrive_expect_tx(bar + st, R::kStage);
+      if (elect_one()) {
+        const uint32_t st = (it + k) % kStages;
+        uint8_t* dst = ring + st * R::kStage;
+        const int64_t codes = (int64_t)k * (kWarps * R::kKc), scales = (int64_t)k * (kWarps * R::kKs);
+        mbar_arrive_expect_tx(bar + st, R::kStage);
+        bulk_load(dst, src_kc + codes, R::kKc, bar + st);
+        bulk_load(dst + R::kKc, src_vc + codes, R::kVc, bar + st);
+        bulk_load(dst + 2 * R::kKc, src_ks + scales, R::kKs, bar + st);
+        bulk_load(dst + 2 * R::kKc + R::kKs, src_vs + scales, R::kVs, bar + st);
+      }
       __syncwarp();
-      if (lane < 4) bulk_load(ring + st * R::kStage + to, from + (int64_t)k * kWarps * bytes, bytes, bar + st);
     };
     for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
 
@@ -296,6 +302,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     // this lane's two rows of the tile: r0 and r0 + 1 (NT = 1: lanes c and c ^ 2 hold the same)
     float o[D / 16][4];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // scores come out of the products as s - m + kLift: the lanes that hold one
+    // part of their own rows start from that (s - 0 before the first m)
+    float shift[2] = {0.f, 0.f};
+    float limit[2] = {-INFINITY, -INFINITY};   // kLift + kMove once there is an m
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     bool ok = true;
@@ -316,7 +326,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
         key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a);
         float acc[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) products<D>(a, q[t], acc[t]);
+        for (int t = 0; t < NT; ++t) {
+          const bool mine = (c >> 1) == t;
+          products<D>(a, q[t], mine ? shift[0] : 0.f, mine ? shift[1] : 0.f, acc[t]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {   // hi + lo, of the lane's own group
           if constexpr (NT == 1) {
@@ -337,15 +350,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
       float top[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmax3(s[0][r], s[0][r + 2], s[1][r]), s[1][r + 2]);
-      if (__any_sync(0xffffffffu, top[0] > m[0] + kMove || top[1] > m[1] + kMove)) {
+      if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], i));
-          const float m1 = fmaxf(m[r], top[r]);
-          const float alpha = m1 == -INFINITY ? 1.f : fast_exp2(m[r] - m1);
+          const float m1 = fmaxf(m[r], top[r] - shift[r]);
+          if (m1 == -INFINITY) continue;
+          const float alpha = fast_exp2(m[r] - m1), more = kLift - m1 - shift[r];
           m[r] = m1;
+          shift[r] = kLift - m1;
+          limit[r] = kLift + kMove;
           l[r] *= alpha;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            s[u][r] += more;
+            s[u][r + 2] += more;
+          }
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             o[j][r] *= alpha;
@@ -353,14 +374,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
           }
         }
       }
-      const float shift0 = m[0] == -INFINITY ? 0.f : kLift - m[0];
-      const float shift1 = m[1] == -INFINITY ? 0.f : kLift - m[1];
       uint32_t pb[2][2];   // P as B fragments: [16 tokens][8 tokens]
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float p0 = fast_exp2(s[u][2 * h] + shift0), p1 = fast_exp2(s[u][2 * h + 1] + shift1);
+          const float p0 = fast_exp2(s[u][2 * h]), p1 = fast_exp2(s[u][2 * h + 1]);
           l[0] += p0;
           l[1] += p1;
           pb[u][h] = transpose8(pack_f16x2(p0, p1));
@@ -448,6 +467,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
 #pragma unroll
     for (int f = 0; f < F; f += 2)
       *reinterpret_cast<float2*>(p.part_o + at * D + f0 + f) = make_float2(acc[f], acc[f + 1]);
+    if (x < x1) {   // the next piece's copies land where the merge was
+      fence_proxy_async_smem();
+      __syncthreads();
+    }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -549,7 +572,7 @@ struct RingW {
   static constexpr int kStagesW = 3;
   static constexpr int kWarp = kStagesW * kStage;
   static constexpr int kRing = kWarps * kWarp;
-  static constexpr int kGroupQ = D / 16 * 32 * 8 + 4 * 4;   // fragments, then the 4 rows' -lse in log2 units
+  static constexpr int kGroupQ = D / 16 * 32 * 8 + 8 * 4;   // fragments, then the 4 rows' -lse in log2 units and 4 zeros
   static constexpr int bytes(int groups) { return kRing + groups * kGroupQ + kWarps * kStagesW * 8 + 32; }
 };
 
@@ -561,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + R::kRing);
   int64_t* where = reinterpret_cast<int64_t*>(bars + kWarps * S);
   uint8_t* smem_q = smem + R::kRing + kWarps * S * 8 + 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
   uint8_t* ring = smem + warp * R::kWarp;
@@ -592,8 +615,6 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
   int b = (int)where[3];
   uint32_t it = 0;
   const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
-  const uint32_t bytes = lane == 0 ? R::kKc : lane == 1 ? R::kKs : R::kW;
-  const uint32_t to = lane == 0 ? 0 : lane == 1 ? R::kKc : R::kKc + R::kKs;
 
   while (x < x1) {
     const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
@@ -608,16 +629,19 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
     const int s_end = (int)min((int64_t)steps, s_begin + (x1 - x));
     x += s_end - s_begin;
     const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
-    // lanes 0..2 each copy from one of the arrays
     const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
-    const uint8_t* from = lane == 0   ? p.c.kc + at0 * (D / 2)
-                          : lane == 1 ? p.c.ks + at0 * (D / 16)
-                                      : reinterpret_cast<const uint8_t*>(p.weights + at0);
+    const uint8_t *src_kc = p.c.kc + at0 * (D / 2), *src_ks = p.c.ks + at0 * (D / 16);
+    const float* src_w = p.weights + at0;
     auto issue = [&](int k) {
-      const uint32_t st = (it + k) % S;
-      if (lane == 0) mbar_arrive_expect_tx(bar + st, R::kKc + R::kKs + (add ? R::kW : 0));
+      if (elect_one()) {
+        const uint32_t st = (it + k) % S;
+        uint8_t* dst = ring + st * R::kStage;
+        mbar_arrive_expect_tx(bar + st, R::kKc + R::kKs + (add ? R::kW : 0));
+        bulk_load(dst, src_kc + (int64_t)k * (kWarps * R::kKc), R::kKc, bar + st);
+        bulk_load(dst + R::kKc, src_ks + (int64_t)k * (kWarps * R::kKs), R::kKs, bar + st);
+        if (add) bulk_load(dst + R::kKc + R::kKs, src_w + (int64_t)k * (kWarps * kStep), R::kW, bar + st);
+      }
       __syncwarp();
-      if (lane < (add ? 3 : 2)) bulk_load(ring + st * R::kStage + to, from + (int64_t)k * kWarps * bytes, bytes, bar + st);
     };
     for (int k = 0; k < min(n_steps, S); ++k) issue(k);
     for (int i = warp; i < groups * 4; i += kWarps) {
@@ -627,7 +651,9 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
         // a row that saw nothing (lse = -inf) and rows behind the last give no weight
         float y = -INFINITY;
         if (i < rows) y = p.w_lse[((int64_t)b * p.heads_q + hk * G + i / p.sq) * p.sq + i % p.sq];
-        reinterpret_cast<float*>(grp + D / 16 * 32 * 8)[i & 3] = y == -INFINITY ? -INFINITY : -y * kLog2e;
+        float* neg = reinterpret_cast<float*>(grp + D / 16 * 32 * 8) + (i & 3);
+        neg[0] = y == -INFINITY ? -INFINITY : -y * kLog2e;
+        neg[4] = 0.f;
       }
     }
     __syncthreads();
@@ -650,13 +676,14 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
         for (int n = 0; n < groups; ++n) {
           const uint8_t* grp = smem_q + n * R::kGroupQ;
           if (groups > 1) load_query_fragments<D>(grp, lane, q);
-          const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + (c & 1) * 8);
+          // -lse for lanes c < 2, zero for the others (their parts are added)
+          const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + c * 8);
           float s[4];
-          products<D>(a, q, s);
+          products<D>(a, q, neg.x, neg.y, s);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);   // hi + lo
-          t0 += fast_exp2(s[0] + neg.x) + fast_exp2(s[1] + neg.y);
-          t1 += fast_exp2(s[2] + neg.x) + fast_exp2(s[3] + neg.y);
+          t0 += fast_exp2(s[0]) + fast_exp2(s[1]);
+          t1 += fast_exp2(s[2]) + fast_exp2(s[3]);
         }
         sum[2 * u] = t0 + __shfl_xor_sync(0xffffffffu, t0, 1);
         sum[2 * u + 1] = t1 + __shfl_xor_sync(0xffffffffu, t1, 1);
