@@ -50,6 +50,18 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// a times the low (high) half of s, which the multiplication takes as an operand modifier.
+__device__ __forceinline__ uint32_t hmul2_low(uint32_t a, uint32_t s) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 t, {lo, lo};\n\tmul.rn.f16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(s));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2_high(uint32_t a, uint32_t s) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 t, {hi, hi};\n\tmul.rn.f16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(s));
+  return r;
+}
+
 // One scale byte in both halves of an fp16 pair.
 __device__ __forceinline__ uint32_t scale_dup(uint32_t byte) { return byte * (0x10001u << 7); }
 

@@ -98,10 +98,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* s
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
 }
 
-// The warp's number, in a form the compiler knows to be the same for all its
-// lanes: what is computed from it (the addresses of the copies) then lives in
-// uniform registers.
-__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+// A value that is the same for all lanes, and the warp's number, in a form that
+// tells the compiler so: what is computed from them (the addresses of the
+// copies) then lives in uniform registers, and branches on them need no
+// reconvergence.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform_warp() { return uniform((int)(threadIdx.x >> 5)); }
 
 // A fragments of 16 tokens' keys (rows g and g + 8 of the tile; lane c's
 // quarter of the features): k-step j covers features c D/4 + 4j .. + 3.
@@ -111,24 +113,22 @@ __device__ __forceinline__ void key_fragments(const uint8_t* kc, const uint8_t* 
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int tok = g + 8 * r;
-    uint32_t w[D / 32], sc[2];
+    uint32_t w[D / 32], sc;   // two scales (head_dim 64: one, in the low half)
     if constexpr (D == 128) {
       const uint4 x = *reinterpret_cast<const uint4*>(kc + tok * 64 + c * 16);
       w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-      const uint32_t s2 = *reinterpret_cast<const uint16_t*>(ks + tok * 8 + c * 2);
-      sc[0] = scale_dup(s2 & 0xffu);
-      sc[1] = scale_dup(s2 >> 8);
+      sc = scale_pair(*reinterpret_cast<const uint16_t*>(ks + tok * 8 + c * 2));
     } else {
       const uint2 x = *reinterpret_cast<const uint2*>(kc + tok * 32 + c * 8);
       w[0] = x.x; w[1] = x.y;
-      sc[0] = sc[1] = scale_dup(ks[tok * 4 + c]);
+      sc = (uint32_t)ks[tok * 4 + c] << 7;
     }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t h[4];
       codes_f16x8(w[i], h);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a[2 * i + (k >> 1)][r + 2 * (k & 1)] = hmul2(h[k], sc[i / 2]);
+      for (int k = 0; k < 4; ++k) a[2 * i + (k >> 1)][r + 2 * (k & 1)] = i < 2 ? hmul2_low(h[k], sc) : hmul2_high(h[k], sc);
     }
   }
 }
@@ -253,22 +253,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
   int64_t x = where[0];
   const int64_t x1 = where[1];
   int64_t begin = where[2];     // flat step where batch element b begins
-  int b = (int)where[3];
+  int b = uniform((int)where[3]);
   uint32_t it = 0;              // steps this warp has begun, over all pieces
 
   while (x < x1) {              // one piece: steps [s_begin, s_end) of one history
-    const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+    const int len = uniform(min(max(__ldg(p.lengths + b), 0), p.c.cap));
     const int steps = (len + kStep - 1) / kStep;
     if (steps == 0 || x >= begin + (int64_t)steps * per) {   // on to the next batch element
       begin += (int64_t)steps * per;
       ++b;
       continue;
     }
-    const int hist = (int)((x - begin) / steps);             // (head, row tile)
+    const int hist = uniform((int)((x - begin) / steps));    // (head, row tile)
     const int hk = hist / row_tiles, row0 = hist % row_tiles * kRows;
     const int bh = b * p.c.heads + hk;
-    const int s_begin = (int)((x - begin) % steps);
-    const int s_end = (int)min((int64_t)steps, s_begin + (x1 - x));
+    const int s_begin = uniform((int)((x - begin) % steps));
+    const int s_end = uniform((int)min((int64_t)steps, s_begin + (x1 - x)));
     const int64_t slot = (int64_t)blockIdx.x + (int64_t)b * per + hist;
     x += s_end - s_begin;
 
@@ -612,21 +612,21 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
   int64_t x = where[0];
   const int64_t x1 = where[1];
   int64_t begin = where[2];
-  int b = (int)where[3];
+  int b = uniform((int)where[3]);
   uint32_t it = 0;
   const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
 
   while (x < x1) {
-    const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+    const int len = uniform(min(max(__ldg(p.lengths + b), 0), p.c.cap));
     const int steps = (len + kStep - 1) / kStep;
     if (steps == 0 || x >= begin + (int64_t)steps * p.c.heads) {
       begin += (int64_t)steps * p.c.heads;
       ++b;
       continue;
     }
-    const int hk = (int)((x - begin) / steps), bh = b * p.c.heads + hk;
-    const int s_begin = (int)((x - begin) % steps);
-    const int s_end = (int)min((int64_t)steps, s_begin + (x1 - x));
+    const int hk = uniform((int)((x - begin) / steps)), bh = b * p.c.heads + hk;
+    const int s_begin = uniform((int)((x - begin) % steps));
+    const int s_end = uniform((int)min((int64_t)steps, s_begin + (x1 - x)));
     x += s_end - s_begin;
     const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
     const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
