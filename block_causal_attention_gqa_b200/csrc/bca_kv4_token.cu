@@ -576,8 +576,12 @@ struct RingW {
   static constexpr int bytes(int groups) { return kRing + groups * kGroupQ + kWarps * kStagesW * 8 + 32; }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const FwdParams4 p, int groups) {
+//
+// kOne: a single group, so that the two halves of a step interleave (the
+// products of a half are one chain) and the queries stay in registers.
+template <int D, bool kOne>
+__global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const FwdParams4 p, int groups_) {
+  const int groups = kOne ? 1 : groups_;
   using R = RingW<D>;
   constexpr int S = R::kStagesW;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -667,27 +671,37 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
       const uint8_t* kc = ring + st * R::kStage;
       const uint8_t* ks = kc + R::kKc;
       const int tok = (s_begin + warp + k * kWarps) * kStep;
-      float sum[4];             // tokens g, g + 8, g + 16, g + 24
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};             // tokens g, g + 8, g + 16, g + 24
+      // one group's weights of 16 tokens
+      auto add_group = [&](const uint32_t (&a)[D / 16][4], const uint8_t* grp, int u) {
+        // -lse for lanes c < 2, zero for the others (their parts are added)
+        const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + c * 8);
+        float y[4];
+        products<D>(a, q, neg.x, neg.y, y);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t a[D / 16][4];
-        key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a);
-        float t0 = 0.f, t1 = 0.f;
-        for (int n = 0; n < groups; ++n) {
-          const uint8_t* grp = smem_q + n * R::kGroupQ;
-          if (groups > 1) load_query_fragments<D>(grp, lane, q);
-          // -lse for lanes c < 2, zero for the others (their parts are added)
-          const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + c * 8);
-          float s[4];
-          products<D>(a, q, neg.x, neg.y, s);
+        for (int i = 0; i < 4; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 2);   // hi + lo
+        sum[2 * u] += fast_exp2(y[0]) + fast_exp2(y[1]);
+        sum[2 * u + 1] += fast_exp2(y[2]) + fast_exp2(y[3]);
+      };
+      if constexpr (kOne) {
+        uint32_t a[2][D / 16][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);   // hi + lo
-          t0 += fast_exp2(s[0]) + fast_exp2(s[1]);
-          t1 += fast_exp2(s[2]) + fast_exp2(s[3]);
+        for (int u = 0; u < 2; ++u) key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a[u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) add_group(a[u], smem_q, u);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t a[D / 16][4];
+          key_fragments<D>(kc + u * 16 * (D / 2), ks + u * 16 * (D / 16), g, c, a);
+          for (int n = 0; n < groups; ++n) {
+            load_query_fragments<D>(smem_q + n * R::kGroupQ, lane, q);
+            add_group(a, smem_q + n * R::kGroupQ, u);
+          }
         }
-        sum[2 * u] = t0 + __shfl_xor_sync(0xffffffffu, t0, 1);
-        sum[2 * u + 1] = t1 + __shfl_xor_sync(0xffffffffu, t1, 1);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
       // every lane of a quad has the four sums: lane c writes token g + 8c
       const float total = c < 2 ? (c == 0 ? sum[0] : sum[1]) : (c == 2 ? sum[2] : sum[3]);
       const int at = g + 8 * c;
@@ -751,19 +765,21 @@ cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s) {
   return one ? token_fwd_d<64, 1>(p, s) : token_fwd_d<64, 2>(p, s);
 }
 
-template <int D>
+template <int D, bool kOne>
 static cudaError_t token_weights_d(const FwdParams4& p, cudaStream_t s) {
   const int rows = p.heads_q / p.c.heads * p.sq, groups = (rows + 3) / 4;
   const int bytes = RingW<D>::bytes(groups);
   static SmemRecord have;
-  const cudaError_t e = allow_smem(kv4_token_weights_kernel<D>, bytes, have);
+  const cudaError_t e = allow_smem(kv4_token_weights_kernel<D, kOne>, bytes, have);
   if (e != cudaSuccess) return e;
-  kv4_token_weights_kernel<D><<<token_ctas(p.c, rows, true), kThreads, bytes, s>>>(p, groups);
+  kv4_token_weights_kernel<D, kOne><<<token_ctas(p.c, rows, true), kThreads, bytes, s>>>(p, groups);
   return cudaGetLastError();
 }
 
 cudaError_t launch_token_weights(const FwdParams4& p, cudaStream_t s) {
-  return p.c.dim == 128 ? token_weights_d<128>(p, s) : token_weights_d<64>(p, s);
+  const bool one = p.heads_q / p.c.heads * p.sq <= 4;
+  if (p.c.dim == 128) return one ? token_weights_d<128, true>(p, s) : token_weights_d<128, false>(p, s);
+  return one ? token_weights_d<64, true>(p, s) : token_weights_d<64, false>(p, s);
 }
 
 }  // namespace kv4
