@@ -112,6 +112,7 @@ cudaError_t launch_read(const ReadParams& p, cudaStream_t s);
 
 // Few query rows per key/value head: the rows in groups of 4, mma.sync.
 int64_t token_piece_rows(const Cache& c, int rows);   // rows of the fwd's part_o / part_ml
+bool token_steps_fit(const Cache& c, int rows);
 cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s);
 cudaError_t launch_token_weights(const FwdParams4& p, cudaStream_t s);
 

@@ -32,6 +32,11 @@ Cache to_cache(const magi_bca_kv4_cache& c) {
   return Cache{c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.batch, c.heads_kv, c.head_dim, c.capacity};
 }
 
+// Which kernels: the token kernels convert the cache once for each 8 rows (fwd)
+// or once in all (weights), the chunk kernels expand it to fp16 first.
+constexpr int kTokenFwdRows = 32;
+constexpr int kTokenWeightRows = 64;
+
 int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
   if (q == nullptr || q->seqlen_q < 1 || q->heads_q < 1) return MAGI_BCA_INVALID_ARG;
   if (!(q->rms_eps >= 0.f) || !(q->softmax_scale >= 0.f) || !std::isfinite(q->softmax_scale) ||
@@ -39,15 +44,12 @@ int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
     return MAGI_BCA_INVALID_ARG;
   if (q->heads_q % c.heads_kv != 0) return MAGI_BCA_UNSUPPORTED;
   if ((int64_t)c.batch * q->heads_q * q->seqlen_q >= (int64_t(1) << 31)) return MAGI_BCA_UNSUPPORTED;
+  const int rows = q->heads_q / c.heads_kv * q->seqlen_q;
+  if (rows <= kTokenWeightRows && !token_steps_fit(to_cache(c), rows)) return MAGI_BCA_UNSUPPORTED;
   return MAGI_BCA_OK;
 }
 
 int rows_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q) { return q.heads_q / c.heads_kv * q.seqlen_q; }
-
-// Which kernels: the token kernels convert the cache once for each 8 rows (fwd)
-// or once in all (weights), the chunk kernels expand it to fp16 first.
-constexpr int kTokenFwdRows = 32;
-constexpr int kTokenWeightRows = 64;
 
 struct Plan {
   bool token = true;

@@ -72,7 +72,7 @@ struct Ring {
   static constexpr int kMerge = kWarps * kRows * kMergeRow * 4;
   static constexpr int kRing = kWarps * kWarp;
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;   // the merge reuses the ring
-  static constexpr int kTotal = kBody + kQ + kWarps * kRows * 8 + kWarps * kStages * 8 + 32;
+  static constexpr int kTotal = kBody + kQ + kWarps * kRows * 8 + kWarps * kStages * 8;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
@@ -155,6 +155,8 @@ __device__ __forceinline__ void load_query_fragments(const uint8_t* smem_q, int 
 }
 
 // ------------------------------------------------- histories laid end to end
+//
+// All in 32 bits: token_steps_fit() has checked the totals.
 __device__ __forceinline__ int steps_of(const FwdParams4& p, int b) {
   const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
   return (len + kStep - 1) / kStep;
@@ -162,54 +164,57 @@ __device__ __forceinline__ int steps_of(const FwdParams4& p, int b) {
 
 // Steps of a batch element's one history, summed over the batch elements below
 // b and over all, by one warp.
-__device__ __forceinline__ void steps_below(const FwdParams4& p, int b, int lane, int64_t& below, int64_t& all) {
+__device__ __forceinline__ void steps_below(const FwdParams4& p, int b, int lane, int& below, int& all) {
   below = all = 0;
   for (int i = lane; i < p.c.batch; i += 32) {
     const int s = steps_of(p, i);
     all += s;
     if (i < b) below += s;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    below += __shfl_xor_sync(0xffffffffu, below, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
+  below = __reduce_add_sync(0xffffffffu, below);
+  all = __reduce_add_sync(0xffffffffu, all);
+}
+
+// `all` steps in n parts, the first all % n of them a step longer.  No more
+// parts than have a step for each warp.
+struct Parts {
+  int n, size, longer;
+  __device__ __forceinline__ Parts(int all, int ctas) {
+    n = min(ctas, (all + kWarps - 1) / kWarps);
+    size = n > 0 ? all / n : 0;
+    longer = all - n * size;
   }
-}
+  __device__ __forceinline__ int begin(int i) const { return i >= n ? n * size + longer : i * size + min(i, longer); }
+  __device__ __forceinline__ int of(int x) const {   // the part that holds step x
+    const int head = longer * (size + 1);
+    return x < head ? x / (size + 1) : longer + (x - head) / size;
+  }
+};
 
-// CTAs that get a part: no more than have a step for each warp.
-__device__ __forceinline__ int parts_of(int64_t all, int ctas) {
-  return (int)min((int64_t)ctas, (all + kWarps - 1) / kWarps);
-}
-
-// First flat step of CTA i's part (the end of the last one's for i >= parts_of).
-__device__ __forceinline__ int64_t part_begin(int64_t all, int i, int ctas) {
-  const int n = parts_of(all, ctas);
-  return i >= n ? all : all * i / n;
-}
-
-// Where the flat step x lies, by one warp: batch element, and the flat step its
-// first history begins at; `all` = steps of all histories.  per: histories of a
-// batch element.  x < all.
-__device__ __forceinline__ void locate(const FwdParams4& p, int64_t x, int per, int lane, int& b, int64_t& begin) {
-  begin = 0;
-  for (int i0 = 0; i0 < p.c.batch; i0 += 32) {
-    int64_t incl = i0 + lane < p.c.batch ? (int64_t)steps_of(p, i0 + lane) * per : 0;
-    const int64_t mine = incl;
+// This CTA's part [x0, x1), the batch element x0 lies in and the flat step that
+// begins at, by one warp.  per: histories of a batch element.
+__device__ __forceinline__ int4 find_part(const FwdParams4& p, int per, int lane) {
+  int none, all;
+  steps_below(p, 0, lane, none, all);
+  const Parts parts(all * per, (int)gridDim.x);
+  const int x0 = parts.begin(blockIdx.x), x1 = parts.begin(blockIdx.x + 1);
+  int begin = 0;
+  for (int i0 = 0; x0 < x1 && i0 < p.c.batch; i0 += 32) {
+    const int mine = i0 + lane < p.c.batch ? steps_of(p, i0 + lane) * per : 0;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, begin + incl > x);
+    const uint32_t hit = __ballot_sync(0xffffffffu, begin + incl > x0);
     if (hit != 0) {
       const int l = __ffs(hit) - 1;
-      b = i0 + l;
-      begin += __shfl_sync(0xffffffffu, incl - mine, l);
-      return;
+      return make_int4(x0, x1, begin + __shfl_sync(0xffffffffu, incl - mine, l), i0 + l);
     }
     begin += __shfl_sync(0xffffffffu, incl, 31);
   }
-  b = p.c.batch;
+  return make_int4(0, 0, 0, 0);
 }
 
 template <int D, int NT>
@@ -221,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
   uint8_t* smem_q = smem + R::kBody;
   float2* smem_ml = reinterpret_cast<float2*>(smem_q + R::kQ);            // [warp][row]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_ml + kWarps * kRows); // [warp][stage]
-  int64_t* where = reinterpret_cast<int64_t*>(bars + kWarps * kStages);
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
@@ -234,41 +238,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {
-    int64_t none, all;
-    steps_below(p, 0, lane, none, all);
-    all *= per;
-    const int64_t x0 = part_begin(all, blockIdx.x, gridDim.x), x1 = part_begin(all, blockIdx.x + 1, gridDim.x);
-    int b = 0;
-    int64_t begin = 0;
-    if (x0 < x1) locate(p, x0, per, lane, b, begin);
-    if (lane == 0) {
-      where[0] = x0;
-      where[1] = x1;
-      where[2] = begin;
-      where[3] = b;
-    }
-  }
-  __syncthreads();
-  int64_t x = where[0];
-  const int64_t x1 = where[1];
-  int64_t begin = where[2];     // flat step where batch element b begins
-  int b = uniform((int)where[3]);
+  __syncwarp();
+  // every warp for itself: the lengths come from the cache, and no one waits
+  const int4 part = find_part(p, per, lane);
+  int x = uniform(part.x);
+  const int x1 = uniform(part.y);
+  int begin = uniform(part.z);  // flat step where batch element b begins
+  int b = uniform(part.w);
   uint32_t it = 0;              // steps this warp has begun, over all pieces
 
   while (x < x1) {              // one piece: steps [s_begin, s_end) of one history
     const int len = uniform(min(max(__ldg(p.lengths + b), 0), p.c.cap));
     const int steps = (len + kStep - 1) / kStep;
-    if (steps == 0 || x >= begin + (int64_t)steps * per) {   // on to the next batch element
-      begin += (int64_t)steps * per;
+    if (steps == 0 || x >= begin + steps * per) {   // on to the next batch element
+      begin += steps * per;
       ++b;
       continue;
     }
-    const int hist = uniform((int)((x - begin) / steps));    // (head, row tile)
+    const int hist = (x - begin) / steps;            // (head, row tile)
     const int hk = hist / row_tiles, row0 = hist % row_tiles * kRows;
     const int bh = b * p.c.heads + hk;
-    const int s_begin = uniform((int)((x - begin) % steps));
-    const int s_end = uniform((int)min((int64_t)steps, s_begin + (x1 - x)));
+    const int s_begin = x - begin - hist * steps;
+    const int s_end = min(steps, s_begin + (x1 - x));
     const int64_t slot = (int64_t)blockIdx.x + (int64_t)b * per + hist;
     x += s_end - s_begin;
 
@@ -486,21 +477,16 @@ __global__ void __launch_bounds__(256) kv4_token_combine_kernel(const FwdParams4
   const int row_tiles = (rows + kRows - 1) / kRows, per = p.c.heads * row_tiles;
   const int bh = (int)(blockIdx.x / rows), row = (int)(blockIdx.x % rows);
   const int b = bh / p.c.heads, hk = bh % p.c.heads;
-  int64_t below, all;
+  int below, all;
   steps_below(p, b, lane, below, all);
   const int steps = steps_of(p, b), hist = hk * row_tiles + row / kRows;
   int n = 0;
   int64_t slot = 0;
-  if (steps > 0) {
-    // the parts that hold a step of [x0, x1)
-    all *= per;
-    const int parts = parts_of(all, ctas);
-    const int64_t x0 = below * per + (int64_t)hist * steps, x1 = x0 + steps;
-    int c0 = (int)(x0 * parts / all), c1 = (int)((x1 * parts + all - 1) / all);
-    while (all * (c0 + 1) / parts <= x0) ++c0;
-    while (all * (c1 - 1) / parts >= x1) --c1;
+  if (steps > 0) {   // the parts that hold a step of the history
+    const Parts parts(all * per, ctas);
+    const int x0 = below * per + hist * steps, c0 = parts.of(x0);
     slot = ((int64_t)b * per + hist + c0) * kRows + row % kRows;
-    n = c1 - c0;
+    n = parts.of(x0 + steps - 1) - c0 + 1;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float mm = -INFINITY, ll = 0.f;
@@ -573,7 +559,7 @@ struct RingW {
   static constexpr int kWarp = kStagesW * kStage;
   static constexpr int kRing = kWarps * kWarp;
   static constexpr int kGroupQ = D / 16 * 32 * 8 + 8 * 4;   // fragments, then the 4 rows' -lse in log2 units and 4 zeros
-  static constexpr int bytes(int groups) { return kRing + groups * kGroupQ + kWarps * kStagesW * 8 + 32; }
+  static constexpr int bytes(int groups) { return kRing + groups * kGroupQ + kWarps * kStagesW * 8; }
 };
 
 //
@@ -586,8 +572,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
   constexpr int S = R::kStagesW;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + R::kRing);
-  int64_t* where = reinterpret_cast<int64_t*>(bars + kWarps * S);
-  uint8_t* smem_q = smem + R::kRing + kWarps * S * 8 + 32;
+  uint8_t* smem_q = smem + R::kRing + kWarps * S * 8;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
@@ -597,40 +582,26 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
     for (int i = 0; i < S; ++i) mbar_init(bar + i, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {
-    int64_t none, all;
-    steps_below(p, 0, lane, none, all);
-    all *= p.c.heads;
-    const int64_t x0 = part_begin(all, blockIdx.x, gridDim.x), x1 = part_begin(all, blockIdx.x + 1, gridDim.x);
-    int b = 0;
-    int64_t begin = 0;
-    if (x0 < x1) locate(p, x0, p.c.heads, lane, b, begin);
-    if (lane == 0) {
-      where[0] = x0;
-      where[1] = x1;
-      where[2] = begin;
-      where[3] = b;
-    }
-  }
-  __syncthreads();
-  int64_t x = where[0];
-  const int64_t x1 = where[1];
-  int64_t begin = where[2];
-  int b = uniform((int)where[3]);
+  __syncwarp();
+  const int4 part = find_part(p, p.c.heads, lane);
+  int x = uniform(part.x);
+  const int x1 = uniform(part.y);
+  int begin = uniform(part.z);
+  int b = uniform(part.w);
   uint32_t it = 0;
   const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
 
   while (x < x1) {
     const int len = uniform(min(max(__ldg(p.lengths + b), 0), p.c.cap));
     const int steps = (len + kStep - 1) / kStep;
-    if (steps == 0 || x >= begin + (int64_t)steps * p.c.heads) {
-      begin += (int64_t)steps * p.c.heads;
+    if (steps == 0 || x >= begin + steps * p.c.heads) {
+      begin += steps * p.c.heads;
       ++b;
       continue;
     }
-    const int hk = uniform((int)((x - begin) / steps)), bh = b * p.c.heads + hk;
-    const int s_begin = uniform((int)((x - begin) % steps));
-    const int s_end = uniform((int)min((int64_t)steps, s_begin + (x1 - x)));
+    const int hk = (x - begin) / steps, bh = b * p.c.heads + hk;
+    const int s_begin = x - begin - hk * steps;
+    const int s_end = min(steps, s_begin + (x1 - x));
     x += s_end - s_begin;
     const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
     const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
@@ -719,21 +690,28 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
 
 int row_tile(int rows) { return rows <= 4 ? 4 : 8; }
 
+int64_t histories(const Cache& c, int rows, bool weights) {
+  const int tile = weights ? rows : row_tile(rows);
+  return (int64_t)c.batch * c.heads * ((rows + tile - 1) / tile);
+}
+
 }  // namespace
 
 // CTAs of the token kernels: as many as run at once (4 an SM, 3 with two row
 // groups), but no more than have a step for each warp if the cache is full.
 int token_ctas(const Cache& c, int rows, bool weights) {
-  const int tile = weights ? rows : row_tile(rows);
-  const int64_t hist = (int64_t)c.batch * c.heads * ((rows + tile - 1) / tile);
-  const int64_t useful = hist * ((c.cap + kStep * kWarps - 1) / (kStep * kWarps));
-  return (int)std::min<int64_t>(useful, 148 * (weights || tile == 4 ? 4 : 3));
+  const int64_t useful = histories(c, rows, weights) * ((c.cap + kStep * kWarps - 1) / (kStep * kWarps));
+  return (int)std::min<int64_t>(useful, 148 * (weights || row_tile(rows) == 4 ? 4 : 3));
 }
 
 // Rows of pieces: (slots) x (rows of a tile).
 int64_t token_piece_rows(const Cache& c, int rows) {
-  const int tile = row_tile(rows);
-  return ((int64_t)c.batch * c.heads * ((rows + tile - 1) / tile) + token_ctas(c, rows, false)) * tile;
+  return (histories(c, rows, false) + token_ctas(c, rows, false)) * row_tile(rows);
+}
+
+// Whether the kernels' 32-bit step numbers can count a full cache.
+bool token_steps_fit(const Cache& c, int rows) {
+  return histories(c, rows, false) * ((c.cap + kStep - 1) / kStep) < (int64_t(1) << 30);
 }
 
 template <int D, int NT>
