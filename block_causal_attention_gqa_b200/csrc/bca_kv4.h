@@ -32,12 +32,13 @@ struct SmemRecord {
 };
 
 template <typename F>
-cudaError_t allow_smem(F* kernel, int bytes, SmemRecord& have) {
+cudaError_t allow_smem(F* kernel, int bytes, SmemRecord& have, bool large_cluster = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && have.bytes[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && large_cluster) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) {
     int was = have.bytes[dev].load();
     while (was < bytes && !have.bytes[dev].compare_exchange_weak(was, bytes)) {

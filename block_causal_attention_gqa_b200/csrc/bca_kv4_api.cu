@@ -72,7 +72,7 @@ Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weig
   p.rows_pad = (int)(((int64_t)rows + 127) / 128 * 128);
   if (p.token) {
     if (!weights) {
-      const size_t n = (size_t)token_piece_rows(cc, rows);
+      const size_t n = (size_t)token_piece_rows(cc, rows);   // 0 for short histories
       p.part_o = take(n * D * 4);
       p.part_ml = take(n * 8);
     }

@@ -158,10 +158,12 @@ def test_evict_arguments():
 
 def test_workspace_sizes():
     lib = bca.library()
-    c = ctypes.byref(cache(batch=1, heads_kv=64, capacity=128))
-    # a single token: pieces of rows to join, far less than the cache; its weights need nothing
-    assert 0 < lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(heads_q=64))) < 1 << 20
-    assert lib.magi_bca_kv4_weights_workspace_size(c, ctypes.byref(query(heads_q=64))) == 0
+    # a single token over short histories needs none, over long ones pieces of
+    # rows to join, far less than the cache; its weights need none
+    for capacity, low, high in ((128, 0, 0), (1 << 17, 1, 1 << 21)):
+        c = ctypes.byref(cache(batch=1, heads_kv=8, capacity=capacity))
+        assert low <= lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(heads_q=24))) <= high
+        assert lib.magi_bca_kv4_weights_workspace_size(c, ctypes.byref(query(heads_q=24))) == 0
     # a chunk: the expanded cache and queries at least
     c = ctypes.byref(cache(batch=2, heads_kv=8, capacity=92160))
     n = lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(seqlen_q=5760, heads_q=24)))

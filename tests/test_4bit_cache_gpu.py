@@ -168,7 +168,10 @@ def test_append_outside_the_cache_is_skipped_and_reported():
 # ----------------------------------------------------------------- attention
 FEW = [(1, 1, 1, 1, 64, 128, [1]), (1, 1, 2, 1, 128, 128, [33]), (2, 1, 4, 2, 128, 512, [512, 0]),
        (3, 1, 8, 8, 64, 256, [255, 1, 129]), (1, 3, 6, 2, 128, 1408, [1301]), (2, 5, 6, 2, 64, 384, [31, 384]),
-       (1, 8, 4, 1, 128, 640, [600]), (1, 1, 24, 8, 128, 9216, [9001]), (4, 2, 10, 5, 64, 128, [5, 64, 65, 128])]
+       (1, 8, 4, 1, 128, 640, [600]), (1, 1, 24, 8, 128, 9216, [9001]), (4, 2, 10, 5, 64, 128, [5, 64, 65, 128]),
+       # histories long enough to be laid end to end over the CTAs (the others take a cluster each)
+       (1, 1, 2, 1, 128, 20480, [20001]), (3, 2, 4, 1, 64, 17536, [17, 0, 17500]), (2, 1, 3, 1, 64, 65536, [65536, 40000]),
+       (5, 1, 2, 2, 128, 16512, [1, 16512, 0, 9000, 333]), (1, 5, 6, 1, 128, 16640, [16639])]
 MANY = [(1, 33, 1, 1, 64, 128, [1]), (1, 40, 2, 1, 128, 384, [257]), (2, 129, 4, 2, 128, 512, [512, 0]),
         (1, 100, 24, 8, 128, 1152, [1050]), (3, 65, 3, 3, 64, 256, [255, 128, 7]), (1, 513, 4, 2, 64, 2560, [2433]),
         (1, 300, 16, 4, 128, 4096, [4096])]
