@@ -20,7 +20,7 @@ DEBUG_LIB = os.path.join(HERE, "libmagi_bca_debug.so")
 SOURCES = ["bca_api.cu", "bca_fwd.cu", "bca_bwd.cu", "bca_bwd_split.cu", "bca_noalloc.cu", "bca_sched.cpp",
            "bca_kv4_api.cu", "bca_kv4_append.cu", "bca_kv4_token.cu", "bca_kv4_chunk.cu", "bca_kv4_evict.cu"]
 DEPS = SOURCES + ["sm100.cuh", "bca_kernels.h", "bca_sched.h", "bca_norm.cuh", "bca_bwd_common.cuh", "bca_mask.cuh",
-                  "bca_kv4.h", "bca_kv4.cuh", "bca_kv4_query.cuh"]
+                  "bca_kv4.h", "bca_kv4.cuh", "bca_kv4_query.cuh", "bca_kv4_rows.cuh"]
 
 
 def nvcc():

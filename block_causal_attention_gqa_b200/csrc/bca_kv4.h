@@ -57,7 +57,7 @@ struct AppendParams {
   int64_t rope_stride;     // elements from one batch element's angles to the next (0: shared)
   int n;
   float eps;
-  int heads_per_warp;
+  int heads_per_warp, head_groups, key_blocks;   // set by launch_append
   int* status;
 };
 
@@ -90,6 +90,7 @@ struct FwdParams4 {
   uint16_t* ql;            //   and low part (weights only)
   uint16_t* kx;            // chunk path: expanded keys [B, H, cap, D] fp16
   uint16_t* vx;            //   and values
+  float* alpha;            // attention, chunk path: factor of a row's scores [B, H, G * Sq]
   int rows_pad;            // weights, chunk path: G * Sq rounded up to 128
   float* neg_lse;          //   -lse in log2 units [B, H, rows_pad], -inf behind the rows
   const float* w_lse;      // weights: [B, Hq, Sq]

@@ -40,7 +40,7 @@ constexpr int kTokenWeightRows = 64;
 int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
   if (q == nullptr || q->seqlen_q < 1 || q->heads_q < 1) return MAGI_BCA_INVALID_ARG;
   if (!(q->rms_eps >= 0.f) || !(q->softmax_scale >= 0.f) || !std::isfinite(q->softmax_scale) ||
-      !std::isfinite(q->rms_eps) || q->rope_batch_stride < 0)
+      !std::isfinite(q->rms_eps) || q->rope_batch_stride < 0 || q->rope_batch_stride % 4 != 0)
     return MAGI_BCA_INVALID_ARG;
   if (q->heads_q % c.heads_kv != 0) return MAGI_BCA_UNSUPPORTED;
   if ((int64_t)c.batch * q->heads_q * q->seqlen_q >= (int64_t(1) << 31)) return MAGI_BCA_UNSUPPORTED;
@@ -55,7 +55,7 @@ struct Plan {
   bool token = true;
   int splits = 1;
   int rows_pad = 0;
-  size_t part_o = 0, part_ml = 0, qh = 0, ql = 0, kx = 0, vx = 0, neg_lse = 0, total = 0;
+  size_t part_o = 0, part_ml = 0, qh = 0, ql = 0, kx = 0, vx = 0, alpha = 0, neg_lse = 0, total = 0;
 };
 
 Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weights) {
@@ -85,6 +85,7 @@ Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weig
       p.neg_lse = take(BH * p.rows_pad * 4);
     } else {
       p.vx = take(BH * c.capacity * D * 2);
+      p.alpha = take(BH * rows * 4);
     }
   }
   if (!p.token && p.splits > 1) {
@@ -115,6 +116,7 @@ FwdParams4 params_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, c
   p.ql = reinterpret_cast<uint16_t*>(w + plan.ql);
   p.kx = reinterpret_cast<uint16_t*>(w + plan.kx);
   p.vx = reinterpret_cast<uint16_t*>(w + plan.vx);
+  p.alpha = reinterpret_cast<float*>(w + plan.alpha);
   p.neg_lse = reinterpret_cast<float*>(w + plan.neg_lse);
   return p;
 }
@@ -143,7 +145,7 @@ int magi_bca_kv4_append(const magi_bca_bf16* k, const magi_bca_bf16* v, const ma
   if (st != MAGI_BCA_OK) return st;
   if (!k || !v || !start || n_tokens < 1 || rope_batch_stride < 0 || !(rms_eps >= 0.f) || !std::isfinite(rms_eps))
     return MAGI_BCA_INVALID_ARG;
-  if (!aligned(k, 16) || !aligned(v, 16)) return MAGI_BCA_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(rope_k, 16) || rope_batch_stride % 4 != 0) return MAGI_BCA_INVALID_ARG;
   if (n_tokens > (1 << 30)) return MAGI_BCA_UNSUPPORTED;
   AppendParams p = {};
   st = device_status_word(&p.status);
@@ -192,7 +194,7 @@ int magi_bca_kv4_fwd(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, co
   if (st != MAGI_BCA_OK) return st;
   if (!q || !lengths || !gamma_q || !gamma_k || !out || (base_out == nullptr) != (base_lse == nullptr))
     return MAGI_BCA_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(base_out, 16)) return MAGI_BCA_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(base_out, 16) || !aligned(rope_q, 16)) return MAGI_BCA_INVALID_ARG;
   if (base_out == out || (lse != nullptr && base_lse == lse)) return MAGI_BCA_INVALID_ARG;
   const Plan plan = plan_of(*cache, *query, false);
   st = check_workspace(plan, workspace, workspace_bytes);
@@ -234,7 +236,7 @@ int magi_bca_kv4_weights(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache
   st = check_query(*cache, query);
   if (st != MAGI_BCA_OK) return st;
   if (!q || !lengths || !lse || !gamma_q || !gamma_k || !weights || !std::isfinite(decay)) return MAGI_BCA_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(weights, 16)) return MAGI_BCA_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(weights, 16) || !aligned(rope_q, 16)) return MAGI_BCA_INVALID_ARG;
   const Plan plan = plan_of(*cache, *query, true);
   st = check_workspace(plan, workspace, workspace_bytes);
   if (st != MAGI_BCA_OK) return st;

@@ -7,348 +7,382 @@
 // arithmetic.  For values it never does: v is bf16, max|v| / 6 and v / s are
 // correctly rounded fp32 quotients, and no fp32 quotient of such operands
 // rounds onto a border it does not lie on.  A key comes out of a rotation and a
-// square root, so its fp32 value carries an error, which is bounded below by
-// 2^-20 (|a| + |b|) r for the pair (a, b) that was rotated (sine and cosine are
-// off by 2 ulp, the three roundings of the rotation by half an ulp of a
-// product each, r by less than 8 ulp).  A row in which some x +- that bound
-// falls on two codes, or some block maximum on two scales, is done again in
-// fp64 by the whole warp; about one row in 300 is.  The codes are those of the
-// exact definition but for values within 1e-14 of a border.
+// square root, so its fp32 value x / s carries an error, bounded for the pair
+// (a, b) that was rotated by 1.25 * 2^-20 (|a| + |b|) r / s: 2^-23 each for sine
+// and cosine and three roundings of 2^-24 in the rotation, 10.5 * 2^-24 for r (9
+// roundings in the sum of squares, halved by the root; two before the root, 4
+// for rsqrtf's 2 ulp, one product) and two in the product with 1 / s.  A row
+// with some x / s +- that bound on two codes, or some block maximum on two
+// scales, has that settled in fp64; about one row in 100 has.  The codes are those
+// of the exact definition but for values within 1e-14 of a border.
 //
-// Layout.  One warp takes a row of the value cache, which holds two tokens,
-// for one head: their two keys and two values, lane l the features [l*E,
-// l*E + E), E = D/32, as the key pre-pass of the forward does; a block's
-// maximum is then over 16/E lanes.  With rotary angles a warp takes several
-// heads, so that a sine and cosine serve them all.
+// Layout.  A lane takes a block: 32 bytes in, 8 bytes of codes and a scale out
+// for a key, 16 bytes for the two tokens that a row of the value cache holds.
+// Nothing is exchanged but the row's sum of squares and the other feature of a
+// rotated pair.  (A lane for 4 features, with the block's maximum by shuffles,
+// took 31 us for 5760 tokens of 8 heads where this takes 16.)  With rotary angles a
+// row's lanes pass over several heads, so that a sine and cosine serve them all.
 //
 // Bound: bytes (4 D read, D + D/8 written per token and head) for chunks;
 // launch latency for single tokens.
 #include <algorithm>
 
-#include "bca_kv4.cuh"
+#include "bca_kv4_rows.cuh"
 
 namespace magi {
 namespace kv4 {
 namespace {
 
-constexpr float kKeyErr = 9.5367431640625e-07f;   // 2^-20
+constexpr float kKeyErr = 1.25f * 9.5367431640625e-07f;   // 1.25 * 2^-20
+constexpr int kThreads = 128;
 
-template <int E>
-__device__ __forceinline__ float block_max(float v) {
-#pragma unroll
-  for (int o = kBlock / E / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-template <int E>
-__device__ __forceinline__ void load_row(const uint16_t* src, int lane, float (&x)[E]) {
-  if constexpr (E == 4) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + lane * 4));
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-  } else {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src + lane * 2));
-    x[0] = bf16_lo(w); x[1] = bf16_hi(w);
-  }
-}
-
-// x / s, correctly rounded, from r = RN(1 / s) (Markstein's division: a
-// quotient estimate and one residual step; the scale has 4 significant bits).
-__device__ __forceinline__ float div_by_scale(float x, float s, float r) {
+// x / y, correctly rounded, from r = RN(1 / y) (Markstein's division: a
+// quotient estimate and one residual step; y is 6 or has 4 significant bits).
+__device__ __forceinline__ float divide(float x, float y, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
+  return fmaf(fmaf(-q, y, x), r, q);
 }
+
+// The scale byte for a block maximum m.
+__device__ __forceinline__ uint32_t scale_of_max(float m) { return encode_scale(divide(m, 6.f, 1.f / 6.f)); }
 
 // NaN -> 0, and into the range the format holds.
 __device__ __forceinline__ float tame(float x) {
   return x == x ? fminf(fmaxf(x, -kTopValue), kTopValue) : 0.f;
 }
 
-// Codes of a lane's E features (E/2 bytes) and the block's scale byte, from
-// features that are exact (values).
-template <int E>
-__device__ __forceinline__ uint32_t encode_exact(const float (&x)[E], uint32_t& scale_byte) {
-  float m = 0.f;
+__device__ __forceinline__ float max_abs(const float (&x)[16]) {
+  float m[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(x[e]));
-  scale_byte = encode_scale(block_max<E>(m) / 6.f);
-  const float s = scale_value(scale_byte);
-  if (scale_byte == 0) return 0;
-  const float r = __frcp_rn(s);
-  uint32_t codes = 0;
+  for (int i = 0; i < 4; ++i) m[i] = fmaxf(fabsf(x[i]), fabsf(x[i + 4]));
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    codes |= encode2(div_by_scale(x[e], s, r), div_by_scale(x[e + 1], s, r)) << (4 * e);
-  return codes;
+  for (int i = 0; i < 4; ++i) m[i] = sm100::fmax3(m[i], fabsf(x[i + 8]), fabsf(x[i + 12]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// A key row in fp64 (by the whole warp; x holds the raw row): the rare rows
-// whose codes the fp32 arithmetic cannot settle.
+// Four bytes to a word.
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// One key row in fp64 by the whole warp, D/32 features a lane (so that the
+// row's sines and cosines, which are what it takes, are spread over all lanes):
+// the lane's codes and its block's scale byte.  near: the scale byte that fp32
+// found, off by one at most.
 template <int D>
-__device__ __noinline__ uint32_t encode_key_f64(const float* x, const float* ang, int lane, float eps,
+__device__ __noinline__ uint32_t encode_key_f64(const uint16_t* row, const float* ang, int lane, float eps, uint32_t near,
                                                 uint32_t* scale_byte) {
-  constexpr int E = D / 32;
-  double ss = 0.;
+  constexpr int E = D / 32, kPer = 16 / E;   // features a lane, lanes a block
+  double x[E], y[E], ss = 0., m = 0.;
 #pragma unroll
-  for (int e = 0; e < E; ++e) ss += (double)x[e] * (double)x[e];
+  for (int e = 0; e < E; ++e) {
+    x[e] = (double)__uint_as_float((uint32_t)__ldg(row + lane * E + e) << 16);
+    ss = fma(x[e], x[e], ss);
+  }
+  double sn[E], cs[E];
+  if (ang != nullptr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sincos_f64((double)__ldg(ang + (lane & 15) * E + e), sn[e], cs[e]);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double norm = sqrt(ss / D + (double)eps);
-  double y[E], m = 0.;
+  // 1 / sqrt by two Newton steps from fp32
+  const double t = fma(ss, 1. / D, (double)eps);
+  double r = (double)rsqrtf((float)t);
+  r = r * fma(-0.5 * t * r, r, 1.5);
+  r = r * fma(-0.5 * t * r, r, 1.5);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     double v = x[e];
     const double other = __shfl_xor_sync(0xffffffffu, v, 16);
-    if (ang != nullptr) {
-      double sn, cs;
-      sincos((double)__ldg(ang + (lane & 15) * E + e), &sn, &cs);
-      v = lane < 16 ? v * cs - other * sn : v * cs + other * sn;
-    }
-    v /= norm;
+    if (ang != nullptr) v = fma(lane < 16 ? -other : other, sn[e], v * cs[e]);
+    v *= r;
     y[e] = v == v ? fmin(fmax(v, (double)-kTopValue), (double)kTopValue) : 0.;
     m = fmax(m, fabs(y[e]));
   }
 #pragma unroll
-  for (int o = kBlock / E / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // the scale: round m / 6 to 4 significant bits, steps of 2^-17 below 2^-14
-  const double want = m / 6.;
-  uint32_t byte;
-  if (want < 6.103515625e-05) {
-    byte = (uint32_t)__double2int_rn(want * 131072.);
-  } else {
-    const int ex = ilogb(want);                              // 2^ex <= want
-    const int mant = __double2int_rn(scalbn(want, 3 - ex));  // 8 .. 16
-    byte = min((uint32_t)((ex + 15) * 8 + (mant - 8)), kTopScaleByte);
+  for (int o = kPer / 2; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // the scale: m against 6 times the midpoints between the bytes around `near`
+  uint32_t byte = near > 0 ? near - 1 : 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double mid = 3. * ((double)scale_value(byte) + (double)scale_value(byte + 1));
+    if (byte < kTopScaleByte && (m > mid || (m == mid && (byte & 1u)))) ++byte;
   }
   *scale_byte = byte;
-  if (byte == 0) return 0;
-  const double s = (double)scale_value(byte);
+  const double rs = byte != 0 ? 1. / (double)scale_value(byte) : 0.;
   uint32_t codes = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const double a = fabs(y[e]) / s;
-    const double step = a < 2. ? 0.5 : a < 4. ? 1. : 2.;
-    const double t = fmin(rint(a / step) * step, 6.);
-    const uint32_t c = t < 2. ? (uint32_t)(t * 2.) : t < 4. ? (uint32_t)t + 2u : (uint32_t)(t * 0.5) + 4u;
-    codes |= (c | (y[e] < 0. ? 8u : 0u)) << (4 * e);
+    const double a = fabs(y[e]) * rs;
+    const double per = a < 2. ? 2. : a < 4. ? 1. : 0.5;
+    const int c = min((int)rint(a * per) + (a < 2. ? 0 : a < 4. ? 2 : 4), 7);
+    codes |= (uint32_t)(c | (y[e] < 0. ? 8 : 0)) << (4 * e);
   }
   return codes;
 }
 
-// Codes and scale byte of one raw key row x (lane's E features); cs, sn: the
-// lane's cosines and sines (rope only).
-template <int D, bool kRope>
-__device__ __forceinline__ uint32_t encode_key(const float (&x)[D / 32], const float (&cs)[D / 32],
-                                               const float (&sn)[D / 32], const float* ang, int lane, float eps,
-                                               uint32_t& scale_byte) {
-  constexpr int E = D / 32;
-  const float r = rms_inv<D>(warp_sumsq_row<E>(x), eps);
-  float y[E], err[E], m = 0.f, me = 0.f;
+// The rows of the warp that `open` names (in any lane of them), again in fp64;
+// row and ang: this lane's row and angles.
+template <int D>
+__device__ __forceinline__ void settle_f64(bool open, const uint16_t* row, const float* ang, int lane, float eps,
+                                           uint2& codes, uint32_t& scale_byte) {
+  using R = RowLanes<D>;
+  constexpr int E = D / 32, kPer = 16 / E;
+  uint32_t which = __ballot_sync(0xffffffffu, open);
+  while (which != 0) {
+    const int owner = __ffs(which) - 1, sub = owner / R::kLanes;
+    which &= ~(((1u << R::kLanes) - 1u) << (sub * R::kLanes));
+    const uint64_t rp = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), owner);
+    const uint64_t ap = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(ang), owner);
+    const uint32_t near = __shfl_sync(0xffffffffu, scale_byte, sub * R::kLanes + lane / kPer);
+    uint32_t byte;
+    const uint32_t part = encode_key_f64<D>(reinterpret_cast<const uint16_t*>(rp), reinterpret_cast<const float*>(ap),
+                                            lane, eps, near, &byte);
+    // back to 16 features a lane
+    const int li = lane % R::kLanes;
+    uint64_t all = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    float v = x[e], mag = fabsf(v);
-    if constexpr (kRope) {
-      const float o = __shfl_xor_sync(0xffffffffu, v, 16);
-      mag += fabsf(o);
-      v = lane < 16 ? rope_first(v, o, cs[e], sn[e]) : rope_second(o, v, cs[e], sn[e]);
+    for (int j = 0; j < kPer; ++j)
+      all |= (uint64_t)__shfl_sync(0xffffffffu, part, li * kPer + j) << (4 * E * j);
+    byte = __shfl_sync(0xffffffffu, byte, li * kPer);
+    if (lane / R::kLanes == sub) {
+      codes = make_uint2((uint32_t)all, (uint32_t)(all >> 32));
+      scale_byte = byte;
     }
-    y[e] = tame(v * r);
-    err[e] = mag * r * kKeyErr;
-    m = fmaxf(m, fabsf(y[e]));
-    me = fmaxf(me, err[e]);
   }
-  m = block_max<E>(m);
-  me = block_max<E>(me);
-  scale_byte = encode_scale(m / 6.f);
-  // a row that is not finite ends here: r is 0 or NaN, y and err 0 or NaN
-  bool unsure = encode_scale(fmaxf(m - me, 0.f) / 6.f) != encode_scale((m + me) / 6.f);
-  const float s = scale_value(scale_byte);
-  const float rs = scale_byte != 0 ? __frcp_rn(s) : 0.f;
-  uint32_t codes = 0, low = 0, high = 0;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float q0 = y[e] * rs, q1 = y[e + 1] * rs, d0 = err[e] * rs, d1 = err[e + 1] * rs;
-    codes |= encode2(q0, q1) << (4 * e);
-    low |= encode2(q0 - d0, q1 - d1) << (4 * e);
-    high |= encode2(q0 + d0, q1 + d1) << (4 * e);
-  }
-  // +0 and -0 stand for the same value
-  unsure = unsure || (low != high && ((low ^ high) & 0x77777777u) != 0);
-  if (__any_sync(0xffffffffu, unsure)) {
-    codes = encode_key_f64<D>(x, kRope ? ang : nullptr, lane, eps, &scale_byte);
-  }
-  return scale_byte != 0 ? codes : 0u;
 }
 
+// Codes and scale byte of a lane's block of one raw key row x (at `row`, its angles at `ang`).
 template <int D, bool kRope>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const AppendParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.z;
+__device__ __forceinline__ uint2 encode_key(const float (&x)[16], const float (&sn)[16], const float (&cs)[16],
+                                            const uint16_t* row, const float* ang, int lane, float eps,
+                                            uint32_t& scale_byte) {
+  const int li = lane % RowLanes<D>::kLanes;
+  const float r = row_rms_inv<D>(x, eps);
+  float y[16], mag[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = x[e];
+  if constexpr (kRope) {
+    rope_block<D>(y, sn, cs, li, mag);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mag[e] = fabsf(x[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = tame(y[e] * r);
+  const float m = max_abs(y);
+  const float me = max_abs(mag) * (r * kKeyErr);
+  scale_byte = scale_of_max(m);
+  // a row that is not finite ends here: r is 0 or NaN, y 0, and the bounds 0 or NaN
+  const bool scale_open = scale_of_max(fmaxf(m - me, 0.f)) != scale_of_max(m + me);
+  const float rs = scale_byte != 0 ? __frcp_rn(scale_value(scale_byte)) : 0.f;
+  const float d = r * rs * kKeyErr;
+  uint32_t low[2], high[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 8 * h + 2 * e;
+      const float q0 = y[i] * rs, q1 = y[i + 1] * rs;
+      lo[e] = encode2(fmaf(-mag[i], d, q0), fmaf(-mag[i + 1], d, q1));
+      hi[e] = encode2(fmaf(mag[i], d, q0), fmaf(mag[i + 1], d, q1));
+    }
+    low[h] = pack_bytes(lo[0], lo[1], lo[2], lo[3]);
+    high[h] = pack_bytes(hi[0], hi[1], hi[2], hi[3]);
+  }
+  uint2 codes = make_uint2(low[0], low[1]);
+  // +0 and -0 stand for the same value
+  const bool open = scale_open || (((low[0] ^ high[0]) | (low[1] ^ high[1])) & 0x77777777u) != 0;
+  settle_f64<D>(open, row, kRope ? ang : nullptr, lane, eps, codes, scale_byte);
+  return scale_byte != 0 ? codes : make_uint2(0, 0);
+}
+
+// Blocks [0, key_blocks * head_groups): keys, kRows tokens a warp, each for
+// heads_per_warp heads.  The others: value rows of two tokens, kRows a warp, for
+// one head.
+template <int D, bool kRope>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendParams p) {
+  using R = RowLanes<D>;
+  const int lane = threadIdx.x & 31, li = lane % R::kLanes, sub = lane / R::kLanes;
+  const int b = blockIdx.z, H = p.c.heads, cap = p.c.cap;
   const int n = p.counts != nullptr ? min(max(__ldg(p.counts + b), 0), p.n) : p.n;
-  const int start = __ldg(p.start + b);
-  const int H = p.c.heads, cap = p.c.cap;
-  const int pair_of_warp = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int64_t start = __ldg(p.start + b);
+  if ((int)blockIdx.x < p.key_blocks * p.head_groups) {
+    const int group = blockIdx.x / p.key_blocks;
+    const int h0 = group * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, H);
+    const int t0 = ((blockIdx.x % p.key_blocks) * (kThreads / 32) + (threadIdx.x >> 5)) * R::kRows;
+    if (t0 >= n) return;
+    const int t = min(t0 + sub, n - 1);   // rows behind the last do its work again, and do not write
+    const int64_t at = start + t;
+    const bool live = t0 + sub < n && at >= 0 && at < cap;
+    if (t0 + sub < n && !live && li == 0 && group == 0) atomicCAS(p.status, 0, (int)kErrPosition);
+    float sn[16] = {}, cs[16] = {};
+    const float* ang = nullptr;
+    if constexpr (kRope) {
+      ang = p.rope + (int64_t)b * p.rope_stride + (int64_t)t * (D / 2);
+      float angles[16];
+      load_angles<D>(ang, li, angles);
+      sincos_row<16>(angles, sn, cs);
+    }
+    const uint16_t* row = p.k + (((int64_t)b * p.n + t) * H + h0) * D;
+    float next[16];
+    load_block(row + li * 16, next);
+    for (int h = h0; h < h1; ++h, row += D) {
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = next[e];
+      if (h + 1 < h1) load_block(row + D + li * 16, next);
+      uint32_t sb;
+      const uint2 codes = encode_key<D, kRope>(x, sn, cs, row, ang, lane, p.eps, sb);
+      if (live) {
+        const int64_t to = ((int64_t)b * H + h) * cap + at;
+        *reinterpret_cast<uint2*>(p.c.kc + to * (D / 2) + li * 8) = codes;
+        p.c.ks[to * (D / 16) + li] = (uint8_t)sb;
+      }
+    }
+    return;
+  }
+  const int block = blockIdx.x - p.key_blocks * p.head_groups, h = block % H;
   // tokens t0, t0 + 1 of the call land in the two halves of cache row `row`
-  const int64_t first_row = start >= 0 ? start / 2 : -((1 - (int64_t)start) / 2);   // floor
-  const int64_t row = first_row + pair_of_warp;
+  const int64_t first_row = start >= 0 ? start / 2 : -((1 - start) / 2);   // floor
+  const int64_t row = first_row + ((int64_t)(block / H) * (kThreads / 32) + (threadIdx.x >> 5)) * R::kRows + sub;
   const int64_t t0 = 2 * row - start;
   bool live[2];
-  bool outside = false;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) live[i] = t0 + i >= 0 && t0 + i < n && 2 * row + i >= 0 && 2 * row + i < cap;
+  if (!live[0] && !live[1]) return;   // no shuffles below
+  float v[2][16];
+  uint32_t sb[2];
+  float s[2], rs[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t t = t0 + i, at = 2 * row + i;
-    live[i] = t >= 0 && t < n;
-    if (live[i] && (at < 0 || at >= cap)) {
-      outside = true;
-      live[i] = false;
-    }
+    // a half that is not written reads the other half's token
+    load_block(p.v + (((int64_t)b * p.n + (live[i] ? t0 + i : t0 + 1 - i)) * H + h) * D + li * 16, v[i]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[i][e] = tame(v[i][e]);
+    sb[i] = scale_of_max(max_abs(v[i]));
+    s[i] = scale_value(sb[i]);
+    rs[i] = sb[i] != 0 ? __frcp_rn(s[i]) : 0.f;
   }
-  if (outside && lane == 0 && blockIdx.y == 0) atomicCAS(p.status, 0, (int)kErrPosition);
-  if (!live[0] && !live[1]) return;
-
-  float cs[2][E] = {}, sn[2][E] = {};
-  const float* ang[2] = {nullptr, nullptr};
-  if constexpr (kRope) {
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ang[i] = p.rope + (int64_t)b * p.rope_stride + (live[i] ? t0 + i : t0 + 1 - i) * (D / 2);
+  for (int k = 0; k < 4; ++k) {
+    uint32_t c[4];
 #pragma unroll
-      for (int e = 0; e < E; ++e) sincosf(__ldg(ang[i] + (lane & 15) * E + e), &sn[i][e], &cs[i][e]);
-    }
+    for (int e = 0; e < 4; ++e)
+      c[e] = encode2(divide(v[0][4 * k + e], s[0], rs[0]), divide(v[1][4 * k + e], s[1], rs[1]));
+    w[k] = pack_bytes(c[0], c[1], c[2], c[3]);
   }
-  const int h0 = blockIdx.y * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, H);
-  for (int h = h0; h < h1; ++h) {
-    float k[2][E], v[2][E];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // a half that is not written reads the other half's token
-      const int64_t src = (((int64_t)b * p.n + (live[i] ? t0 + i : t0 + 1 - i)) * H + h) * D;
-      load_row<E>(p.k + src, lane, k[i]);
-      load_row<E>(p.v + src, lane, v[i]);
-    }
-    const int64_t bh = (int64_t)b * H + h;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t sb;
-      const uint32_t codes = encode_key<D, kRope>(k[i], cs[i], sn[i], ang[i], lane, p.eps, sb);
-      if (live[i]) {   // warp-uniform
-        const int64_t at = bh * cap + 2 * row + i;
-        if constexpr (E == 4)
-          reinterpret_cast<uint16_t*>(p.c.kc + at * (D / 2))[lane] = (uint16_t)codes;
-        else
-          (p.c.kc + at * (D / 2))[lane] = (uint8_t)codes;
-        if (lane % (kBlock / E) == 0) (p.c.ks + at * (D / kBlock))[lane / (kBlock / E)] = (uint8_t)sb;
-      }
-    }
-    uint32_t vcodes[2], vsb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = tame(v[i][e]);
-      vcodes[i] = encode_exact<E>(v[i], vsb[i]);
-    }
-    // byte of feature e: token 2 row in the low half, token 2 row + 1 in the high half
-    const int64_t vrow = bh * (cap / 2) + row;
-    uint8_t* dst = p.c.vc + vrow * D + lane * E;
-    uint8_t* sdst = p.c.vs + (vrow * (D / kBlock) + lane / (kBlock / E)) * 2;
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      bytes |= ((vcodes[0] >> (4 * e)) & 15u) << (8 * e);
-      bytes |= ((vcodes[1] >> (4 * e)) & 15u) << (8 * e + 4);
-    }
-    const uint32_t keep = live[0] && live[1] ? 0u : live[0] ? 0xf0f0f0f0u : 0x0f0f0f0fu;
-    if constexpr (E == 4) {
-      uint32_t* d = reinterpret_cast<uint32_t*>(dst);
-      *d = keep == 0 ? bytes : (*d & keep) | (bytes & ~keep);
-    } else {
-      uint16_t* d = reinterpret_cast<uint16_t*>(dst);
-      *d = (uint16_t)(keep == 0 ? bytes : (*d & keep) | (bytes & ~keep));
-    }
-    if (lane % (kBlock / E) == 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (live[i]) sdst[i] = (uint8_t)vsb[i];
-    }
-  }
-}
-
-// bf16 values of E codes (E/2 bytes) of one scale.
-template <int E>
-__device__ __forceinline__ void store_values(uint16_t* dst, uint32_t codes, uint32_t scale, int lane) {
-  if constexpr (E == 4) {
-    uint2 w;
-    w.x = f16x2_to_bf16x2(hmul2(codes_f16x2(codes & 0xffu), scale));
-    w.y = f16x2_to_bf16x2(hmul2(codes_f16x2((codes >> 8) & 0xffu), scale));
-    reinterpret_cast<uint2*>(dst)[lane] = w;
+  const int64_t vrow = ((int64_t)b * H + h) * (cap / 2) + row;
+  uint4* dst = reinterpret_cast<uint4*>(p.c.vc + vrow * D + li * 16);
+  uint8_t* sdst = p.c.vs + (vrow * (D / 16) + li) * 2;
+  if (live[0] && live[1]) {
+    *dst = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint16_t*>(sdst) = (uint16_t)(sb[0] | sb[1] << 8);
   } else {
-    reinterpret_cast<uint32_t*>(dst)[lane] = f16x2_to_bf16x2(hmul2(codes_f16x2(codes & 0xffu), scale));
+    const uint32_t keep = live[0] ? 0xf0f0f0f0u : 0x0f0f0f0fu;
+    const uint4 old = *dst;
+    *dst = make_uint4((old.x & keep) | (w[0] & ~keep), (old.y & keep) | (w[1] & ~keep), (old.z & keep) | (w[2] & ~keep),
+                      (old.w & keep) | (w[3] & ~keep));
+    sdst[live[0] ? 0 : 1] = (uint8_t)sb[live[0] ? 0 : 1];
   }
 }
 
-// One warp per (batch element, token, head); a position outside the cache
-// gives zeros.
+// A lane's 16 bf16 values from pairs of codes in order.
+__device__ __forceinline__ void store_block(uint16_t* dst, const uint32_t (&h)[8]) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  d[0] = make_uint4(f16x2_to_bf16x2(h[0]), f16x2_to_bf16x2(h[1]), f16x2_to_bf16x2(h[2]), f16x2_to_bf16x2(h[3]));
+  d[1] = make_uint4(f16x2_to_bf16x2(h[4]), f16x2_to_bf16x2(h[5]), f16x2_to_bf16x2(h[6]), f16x2_to_bf16x2(h[7]));
+}
+
+// A lane takes a block of a value row's two tokens, and the same tokens' keys.
+// A position outside the cache gives zeros.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const ReadParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int H = p.c.heads, cap = p.c.cap;
-  const int64_t rows = (int64_t)p.c.batch * p.n * H;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
-  for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
-    const int h = (int)(r % H);
-    const int64_t bt = r / H;
-    const int b = (int)(bt / p.n);
-    const int64_t at = (p.start != nullptr ? (int64_t)__ldg(p.start + b) : 0) + bt % p.n;
-    uint32_t kc = 0, vc = 0, ks = 0, vs = 0;
-    if (at >= 0 && at < cap) {
-      const int64_t krow = ((int64_t)b * H + h) * cap + at, vrow = ((int64_t)b * H + h) * (cap / 2) + at / 2;
-      const int blk = lane / (kBlock / E), half = (int)(at & 1);
-      ks = p.c.ks[krow * (D / kBlock) + blk];
-      vs = p.c.vs[(vrow * (D / kBlock) + blk) * 2 + half];
-      if constexpr (E == 4) {
-        kc = reinterpret_cast<const uint16_t*>(p.c.kc + krow * (D / 2))[lane];
-        const uint32_t w = (reinterpret_cast<const uint32_t*>(p.c.vc + vrow * D)[lane] >> (4 * half)) & 0x0f0f0f0fu;
-        vc = (w | (w >> 4)) & 0x00ff00ffu;   // codes 0, 1 in byte 0, codes 2, 3 in byte 2
-        vc = (vc | (vc >> 8)) & 0xffffu;
-      } else {
-        kc = (p.c.kc + krow * (D / 2))[lane];
-        const uint32_t w = (reinterpret_cast<const uint16_t*>(p.c.vc + vrow * D)[lane] >> (4 * half)) & 0x0f0fu;
-        vc = (w | (w >> 4)) & 0xffu;
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadParams p) {
+  constexpr int kLanes = D / 16;
+  const int H = p.c.heads, cap = p.c.cap, b = blockIdx.z;
+  const int64_t start = p.start != nullptr ? (int64_t)__ldg(p.start + b) : 0;
+  const int64_t first_row = start >= 0 ? start / 2 : -((1 - start) / 2);   // floor
+  // items of a batch element: (row, head, lane), so that neighbours write neighbouring features
+  const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int li = (int)(item % kLanes), h = (int)(item / kLanes % H);
+  const int64_t row = first_row + item / (kLanes * H);
+  const int64_t t0 = 2 * row - start;
+  if (t0 >= p.n) return;
+  const bool inside = row >= 0 && row < cap / 2;
+  uint4 vc = make_uint4(0, 0, 0, 0);
+  uint2 kc[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+  uint32_t vs = 0, ks[2] = {0, 0};
+  if (inside) {
+    const int64_t bh = (int64_t)b * H + h, vrow = bh * (cap / 2) + row, krow = bh * cap + 2 * row;
+    vc = *reinterpret_cast<const uint4*>(p.c.vc + vrow * D + li * 16);
+    vs = *reinterpret_cast<const uint16_t*>(p.c.vs + (vrow * (D / 16) + li) * 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kc[i] = *reinterpret_cast<const uint2*>(p.c.kc + (krow + i) * (D / 2) + li * 8);
+      ks[i] = p.c.ks[(krow + i) * (D / 16) + li];
+    }
+  }
+  uint32_t even[8], odd[8];   // the two tokens' values in pairs of features
+  {
+    const uint32_t w[4] = {vc.x, vc.y, vc.z, vc.w}, s = scale_pair(vs);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t x[4];
+      codes_f16x8(w[k], x);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const uint32_t a = hmul2(x[e], s), c = hmul2(x[e + 1], s);
+        even[2 * k + e / 2] = __byte_perm(a, c, 0x5410);
+        odd[2 * k + e / 2] = __byte_perm(a, c, 0x7632);
       }
     }
-    store_values<E>(p.k + r * D, kc, scale_dup(ks), lane);
-    store_values<E>(p.v + r * D, vc, scale_dup(vs), lane);
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t t = t0 + i;
+    if (t < 0 || t >= p.n) continue;
+    const int64_t at = (((int64_t)b * p.n + t) * H + h) * D + li * 16;
+    store_block(p.v + at, i ? odd : even);
+    uint32_t x[8];
+    codes_f16x8(kc[i].x, reinterpret_cast<uint32_t(&)[4]>(x[0]));
+    codes_f16x8(kc[i].y, reinterpret_cast<uint32_t(&)[4]>(x[4]));
+    const uint32_t s = scale_dup(ks[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = hmul2(x[e], s);
+    store_block(p.k + at, x);
+  }
+}
+
+template <int D, bool kRope>
+cudaError_t append_d(AppendParams p, cudaStream_t s) {
+  constexpr int per_block = kThreads / 32 * RowLanes<D>::kRows;
+  p.key_blocks = (p.n + per_block - 1) / per_block;
+  const int value_blocks = (p.n / 2 + 1 + per_block - 1) / per_block;   // rows of two that n tokens can touch
+  // Lanes that pass over several heads save sines and cosines (5760 tokens of 8
+  // heads: 22.6 us with one head a pass, 19.0 with 2, 16.9 with 4, 16.0 with 8);
+  // with few tokens the heads are spread over warps instead, for latency.
+  p.heads_per_warp = kRope && (int64_t)p.key_blocks * p.c.batch >= 148 ? 8 : 1;
+  p.head_groups = (p.c.heads + p.heads_per_warp - 1) / p.heads_per_warp;
+  const dim3 grid(p.key_blocks * p.head_groups + value_blocks * p.c.heads, 1, p.c.batch);
+  kv4_append_kernel<D, kRope><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p0, cudaStream_t s) {
-  AppendParams p = p0;
-  if (p.n <= 0) return cudaSuccess;
-  const int pairs = p.n / 2 + 1;   // rows of two tokens that n tokens can touch
-  // A warp that takes several heads saves sines and cosines; with few tokens the
-  // heads are spread over warps instead, for latency.
-  p.heads_per_warp = p.rope != nullptr && (int64_t)pairs * p.c.batch >= 2048 ? 4 : 1;
-  const dim3 grid((pairs + 7) / 8, (p.c.heads + p.heads_per_warp - 1) / p.heads_per_warp, p.c.batch);
-  const bool rope = p.rope != nullptr;
-  if (p.c.dim == 128) {
-    if (rope) kv4_append_kernel<128, true><<<grid, 256, 0, s>>>(p);
-    else kv4_append_kernel<128, false><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (rope) kv4_append_kernel<64, true><<<grid, 256, 0, s>>>(p);
-    else kv4_append_kernel<64, false><<<grid, 256, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
+  if (p.c.dim == 128) return p.rope != nullptr ? append_d<128, true>(p, s) : append_d<128, false>(p, s);
+  return p.rope != nullptr ? append_d<64, true>(p, s) : append_d<64, false>(p, s);
 }
 
 cudaError_t launch_read(const ReadParams& p, cudaStream_t s) {
-  const int64_t rows = (int64_t)p.c.batch * p.n * p.c.heads;
-  if (rows <= 0) return cudaSuccess;
-  const int blocks = (int)std::min<int64_t>((rows + 7) / 8, 148 * 64);
-  if (p.c.dim == 128) kv4_read_kernel<128><<<blocks, 256, 0, s>>>(p);
-  else kv4_read_kernel<64><<<blocks, 256, 0, s>>>(p);
+  const int64_t items = ((int64_t)p.n / 2 + 1) * p.c.heads * (p.c.dim / 16);
+  const dim3 grid((unsigned)((items + kThreads - 1) / kThreads), 1, p.c.batch);
+  if (p.c.dim == 128) kv4_read_kernel<128><<<grid, kThreads, 0, s>>>(p);
+  else kv4_read_kernel<64><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -29,6 +29,7 @@
 
 #include "bca_kv4.cuh"
 #include "bca_kv4_query.cuh"
+#include "bca_kv4_rows.cuh"
 
 namespace magi {
 namespace kv4 {
@@ -58,38 +59,88 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool o
 
 // ------------------------------------------------------------------- expand
 //
-// Blocks [0, fold_blocks): folded queries, one warp a row (and, for the
-// weights, -lse in log2 units, padded with -inf to whole tiles).  The rest:
-// keys and values of the tokens below the length, rounded up to a tile of 128
-// (zeros there), in items of one key block (16 features of a token) or one
-// value block (8 features of two tokens).
+// Blocks [0, fold_blocks): folded queries, 16 features a lane, a query token's
+// heads of one group one after another (they share its sines and cosines).  For
+// the attention a query is one fp16 number a feature, and the row gets the
+// factor alpha = (q . q) / (q . q16) that makes its rounding harmless to first
+// order: the errors of a row's scores then add up to nothing over keys that lie
+// about the query the way the softmax weights them, so that the lse is good to
+// 1e-7 where it was to 2e-6 (the factor costs nothing: it multiplies where the
+// reference is subtracted).  For the weights it is two numbers, hi + lo, and
+// -lse in log2 units goes along, padded with -inf to whole tiles.
+//
+// The other blocks: keys and values of the tokens below the length, rounded up
+// to a tile of 128 (zeros there), in items of one key block (16 features of a
+// token) or one value block (8 features of two tokens).
 template <int D, bool kValues, bool kLow>
 __global__ void __launch_bounds__(256) kv4_expand_kernel(const FwdParams4 p, int fold_blocks) {
   const int lane = threadIdx.x & 31;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
   const int BH = p.c.batch * p.c.heads;
   if ((int)blockIdx.x < fold_blocks) {
-    const int rows_pad = kLow ? p.rows_pad : rows;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < (int64_t)BH * rows_pad;
-         r += (int64_t)fold_blocks * 8) {
-      const int bh = (int)(r / rows_pad), row = (int)(r % rows_pad);
-      const int b = bh / p.c.heads, hk = bh % p.c.heads;
-      if (row < rows) {
-        uint32_t hi[D / 64], lo[D / 64];
-        fold_query<D>(p, b, hk, G, row, rows, lane, hi, lo);
-        const int64_t at = ((int64_t)bh * rows + row) * D + lane * (D / 32);
-        if constexpr (D == 128) {
-          *reinterpret_cast<uint2*>(p.qh + at) = make_uint2(hi[0], hi[1]);
-          if (kLow) *reinterpret_cast<uint2*>(p.ql + at) = make_uint2(lo[0], lo[1]);
-        } else {
-          *reinterpret_cast<uint32_t*>(p.qh + at) = hi[0];
-          if (kLow) *reinterpret_cast<uint32_t*>(p.ql + at) = lo[0];
+    using R = RowLanes<D>;
+    const int li = lane % R::kLanes, sub = lane / R::kLanes;
+    const int64_t items = (int64_t)BH * p.sq;    // (query token, head group)
+    const int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * R::kRows;
+    if (i0 < items) {   // the same for the warp; rows behind the last repeat it and do not write
+      const int64_t item = min(i0 + sub, items - 1);
+      const bool live = i0 + sub < items;
+      const int hk = (int)(item % p.c.heads), i = (int)(item / p.c.heads % p.sq), b = (int)(item / p.c.heads / p.sq);
+      float gain[16], sn[16], cs[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) gain[e] = qscale_of(p.gamma_q, p.gamma_k, p.scale_log2, li * 16 + e);
+      if (p.rope != nullptr) {
+        float angles[16];
+        load_angles<D>(p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2), li, angles);
+        sincos_row<16>(angles, sn, cs);
+      }
+      for (int g = 0; g < G; ++g) {
+        float x[16], mag[16];
+        load_block(p.q + (((int64_t)b * p.sq + i) * p.heads_q + hk * G + g) * D + li * 16, x);
+        const float r = row_rms_inv<D>(x, p.eps);
+        if (p.rope != nullptr) rope_block<D>(x, sn, cs, li, mag);
+        uint32_t hi[8], lo[8];
+        float qq = 0.f, q16 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float a = x[e] * r * gain[e], c = x[e + 1] * r * gain[e + 1];
+          hi[e / 2] = pack_f16x2(a, c);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[e / 2]));
+          if constexpr (kLow) {
+            lo[e / 2] = pack_f16x2(a - back.x, c - back.y);
+          } else {
+            // q . q = q . q16 + q . (q - q16): the second sum is the small one
+            q16 = fmaf(a, back.x, fmaf(c, back.y, q16));
+            qq = fmaf(a, a - back.x, fmaf(c, c - back.y, qq));
+          }
+        }
+        const int64_t row = ((int64_t)b * p.c.heads + hk) * rows + (int64_t)g * p.sq + i;
+        if constexpr (!kLow) {
+#pragma unroll
+          for (int o = 1; o < R::kLanes; o <<= 1) {
+            q16 += __shfl_xor_sync(0xffffffffu, q16, o);
+            qq += __shfl_xor_sync(0xffffffffu, qq, o);
+          }
+          if (live && li == 0) p.alpha[row] = q16 > 0.f ? 1.f + qq / q16 : 1.f;
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.qh + row * D + li * 16);
+          dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          dst[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          if constexpr (kLow) {
+            uint4* low = reinterpret_cast<uint4*>(p.ql + row * D + li * 16);
+            low[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            low[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          }
         }
       }
-      if (kLow && lane == 0) {
+    }
+    if constexpr (kLow) {
+      for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < (int64_t)BH * p.rows_pad; r += (int64_t)fold_blocks * 256) {
+        const int bh = (int)(r / p.rows_pad), row = (int)(r % p.rows_pad);
         // rows behind the last, and rows that saw nothing, give no weight
         const float x = row < rows ? p.w_lse[(int64_t)bh * rows + row] : -INFINITY;
-        p.neg_lse[(int64_t)bh * rows_pad + row] = x == -INFINITY ? -INFINITY : -x * kLog2e;
+        p.neg_lse[r] = x == -INFINITY ? -INFINITY : -x * kLog2e;
       }
     }
     return;
@@ -312,6 +363,8 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const int bar_id = 1 + s;
       const int row = m0 + s * 128 + r;
       bool ok = true;
+      const float scale = row < rows ? p.alpha[(int64_t)bh * rows + row] : 1.f;   // of the row's scores
+      const uint64_t scale2 = f2_pack(scale, scale);
       float m_ref = -INFINITY, l_sum = 0.f;
       for (int j = 0; j < n_vis; ++j) {
         ok = warp_wait(&bars->s_full[s], j & 1, ok, p.status, kErrSFull);
@@ -358,8 +411,8 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               mx[2 * i] = fmax3(mx[2 * i], a0, b0);
               mx[2 * i + 1] = fmax3(mx[2 * i + 1], a1, b1);
             }
-          const float m_tile = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          const float m_tile = scale * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
           float alpha = 1.f;
           if (m_tile > m_ref + kMove) {
             alpha = fast_exp2(m_ref - m_tile);
@@ -375,7 +428,7 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const uint64_t a2 = f2_add(x2[c * 16 + i], shift);
+                const uint64_t a2 = f2_fma(x2[c * 16 + i], scale2, shift);
                 float p0, p1;
                 if (decltype(use_poly)::value && (i & 3) == 3) {
                   exp2_poly_pair(a2, p0, p1);
@@ -657,8 +710,8 @@ __global__ void __launch_bounds__(256) kv4_weights_sum_kernel(const FwdParams4 p
 
 template <int D>
 cudaError_t expand_d(const FwdParams4& p, bool values, bool low, cudaStream_t s) {
-  const int64_t rows = (int64_t)p.c.batch * p.c.heads * (low ? p.rows_pad : p.heads_q / p.c.heads * p.sq);
-  const int fold = (int)std::min<int64_t>((rows + 7) / 8, 148 * 16);
+  const int64_t items = (int64_t)p.c.batch * p.c.heads * p.sq;
+  const int fold = (int)((items + 8 * RowLanes<D>::kRows - 1) / (8 * RowLanes<D>::kRows));
   const int64_t tiles = (int64_t)p.c.batch * p.c.heads * ((p.c.cap + 127) / 128);
   const int blocks = fold + (int)std::min<int64_t>(tiles, 148 * 16);
   if (values) kv4_expand_kernel<D, true, false><<<blocks, 256, 0, s>>>(p, fold);

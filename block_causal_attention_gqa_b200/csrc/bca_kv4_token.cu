@@ -607,7 +607,7 @@ struct RingW {
   static constexpr int kStagesW = 3;
   static constexpr int kWarp = kStagesW * kStage;
   static constexpr int kRing = kWarps * kWarp;
-  static constexpr int kGroupQ = D / 16 * 32 * 8 + 8 * 4;   // fragments, then the 4 rows' -lse in log2 units and 4 zeros
+  static constexpr int kGroupQ = D / 16 * 32 * 8 + 4 * 4;   // fragments, then the 4 rows' -lse in log2 units
   static constexpr int bytes(int groups) { return kRing + groups * kGroupQ + kWarps * kStagesW * 8; }
 };
 
@@ -675,9 +675,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
         // a row that saw nothing (lse = -inf) and rows behind the last give no weight
         float y = -INFINITY;
         if (i < rows) y = p.w_lse[((int64_t)b * p.heads_q + hk * G + i / p.sq) * p.sq + i % p.sq];
-        float* neg = reinterpret_cast<float*>(grp + D / 16 * 32 * 8) + (i & 3);
-        neg[0] = y == -INFINITY ? -INFINITY : -y * kLog2e;
-        neg[4] = 0.f;
+        reinterpret_cast<float*>(grp + D / 16 * 32 * 8)[i & 3] = y == -INFINITY ? -INFINITY : -y * kLog2e;
       }
     }
     __syncthreads();
@@ -694,14 +692,15 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
       float sum[4] = {0.f, 0.f, 0.f, 0.f};             // tokens g, g + 8, g + 16, g + 24
       // one group's weights of 16 tokens
       auto add_group = [&](const uint32_t (&a)[D / 16][4], const uint8_t* grp, int u) {
-        // -lse for lanes c < 2, zero for the others (their parts are added)
-        const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + c * 8);
+        // -lse comes in fp32 arithmetic: as the products' start value it would cost
+        // them the bits below its own last one (1.7e-6 against 2e-7 in the weights)
+        const float2 neg = *reinterpret_cast<const float2*>(grp + D / 16 * 32 * 8 + (c & 1) * 8);
         float y[4];
-        products<D>(a, q, neg.x, neg.y, y);
+        products<D>(a, q, 0.f, 0.f, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 2);   // hi + lo
-        sum[2 * u] += fast_exp2(y[0]) + fast_exp2(y[1]);
-        sum[2 * u + 1] += fast_exp2(y[2]) + fast_exp2(y[3]);
+        sum[2 * u] += fast_exp2(y[0] + neg.x) + fast_exp2(y[1] + neg.y);
+        sum[2 * u + 1] += fast_exp2(y[2] + neg.x) + fast_exp2(y[3] + neg.y);
       };
       if constexpr (kOne) {
         uint32_t a[2][D / 16][4];

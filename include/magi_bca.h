@@ -343,7 +343,8 @@ typedef struct {
   int32_t heads_q;            /* heads_q % heads_kv == 0 */
   float softmax_scale;        /* 0 selects 1/sqrt(head_dim) */
   float rms_eps;              /* >= 0 */
-  int64_t rope_batch_stride;  /* elements from one batch element's angles to the next; 0 = shared */
+  int64_t rope_batch_stride;  /* elements from one batch element's angles to the next (a multiple of 4; the
+                               * angles are 16-byte aligned); 0 = shared */
 } magi_bca_kv4_query;
 
 /* Quantises k, v [batch, n_tokens, heads_kv, head_dim] bf16 into the slots
@@ -351,7 +352,8 @@ typedef struct {
  * are device int32 [batch]; counts (NULL: n_tokens everywhere) is how many of
  * the tokens are real, the rest is padding and not written.  rope_k [n_tokens,
  * head_dim/2] (or one such table for each batch element, rope_batch_stride
- * apart) are the tokens' angles, or NULL.  Overwriting slots is allowed.  A
+ * apart, a multiple of 4) are the tokens' angles, 16-byte aligned, or NULL.  Angles are taken in fp32 up to
+ * 10^9 in magnitude.  Overwriting slots is allowed.  A
  * token whose slot is outside the cache is not written and sets
  * MAGI_BCA_DEVICE_CHECK in the device status word. */
 int magi_bca_kv4_append(const magi_bca_bf16* k, const magi_bca_bf16* v, const magi_bca_kv4_cache* cache,

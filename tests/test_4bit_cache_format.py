@@ -7,7 +7,6 @@ import pytest
 import torch
 
 import block_causal_attention_gqa_b200 as bca
-from block_causal_attention_gqa_b200.kv4 import CacheStruct, QueryStruct
 from tests import kv4_reference as ref
 
 OK, INVALID, UNSUPPORTED, TOO_SMALL = 0, -1, -2, -4
@@ -50,16 +49,35 @@ def test_pack_and_unpack_agree():
 P = 1 << 20   # a 16-byte aligned address that is never read
 
 
+class CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + [
+        (n, ctypes.c_int32) for n in ("batch", "heads_kv", "head_dim", "capacity")]
+
+
+class QueryStruct(ctypes.Structure):
+    _fields_ = [("seqlen_q", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("rms_eps", ctypes.c_float), ("rope_batch_stride", ctypes.c_int64)]
+
+
 def cache(**kw):
+    """The C struct's bytes, as the binding passes it."""
     f = dict(k_codes=P, k_scales=P, v_codes=P, v_scales=P, batch=1, heads_kv=2, head_dim=128, capacity=256)
     f.update(kw)
-    return CacheStruct(*[f[n] for n, _ in CacheStruct._fields_])
+    return bytes(CacheStruct(*[f[n] for n, _ in CacheStruct._fields_]))
 
 
 def query(**kw):
     f = dict(seqlen_q=1, heads_q=4, softmax_scale=0.0, rms_eps=1e-6, rope_batch_stride=0)
     f.update(kw)
-    return QueryStruct(*[f[n] for n, _ in QueryStruct._fields_])
+    return bytes(QueryStruct(*[f[n] for n, _ in QueryStruct._fields_]))
+
+
+def test_the_bindings_structs_are_the_c_compilers():
+    from block_causal_attention_gqa_b200 import kv4
+    assert kv4._CACHE.size == ctypes.sizeof(CacheStruct) and kv4._QUERY.size == ctypes.sizeof(QueryStruct)
+    assert kv4._CACHE.pack(P, 2 * P, 3 * P, 4 * P, 1, 2, 64, 128) == cache(
+        k_codes=P, k_scales=2 * P, v_codes=3 * P, v_scales=4 * P, batch=1, heads_kv=2, head_dim=64, capacity=128)
+    assert kv4._QUERY.pack(3, 4, 0.5, 1e-5, 64) == query(seqlen_q=3, heads_q=4, softmax_scale=0.5, rms_eps=1e-5, rope_batch_stride=64)
 
 
 BAD_CACHES = [(dict(k_codes=None), INVALID), (dict(v_scales=None), INVALID), (dict(batch=0), INVALID),
@@ -72,9 +90,8 @@ def with_bad_cache(c):
     """A call of each entry point with a cache that has to be refused (the
     pointers must never be read: on a machine with a GPU that would fault)."""
     lib = bca.library()
-    c = ctypes.byref(c) if c is not None else None
-    good = ctypes.byref(cache(k_codes=2 * P, k_scales=2 * P, v_codes=2 * P, v_scales=2 * P))
-    q = ctypes.byref(query())
+    good = cache(k_codes=2 * P, k_scales=2 * P, v_codes=2 * P, v_scales=2 * P)
+    q = query()
     return [lib.magi_bca_kv4_append(P, P, c, P, None, 1, None, 0, 1e-6, None),
             lib.magi_bca_kv4_read(c, P, 1, P, P, None),
             lib.magi_bca_kv4_fwd(P, c, P, P, P, None, None, None, P, P, P, 1 << 40, q, None),
@@ -95,29 +112,30 @@ def test_a_null_cache_is_refused():
                                         (dict(heads_q=5), UNSUPPORTED), (dict(rms_eps=-1.0), INVALID),
                                         (dict(rms_eps=float("nan")), INVALID), (dict(softmax_scale=-1.0), INVALID),
                                         (dict(softmax_scale=float("inf")), INVALID),
-                                        (dict(rope_batch_stride=-1), INVALID),
+                                        (dict(rope_batch_stride=-1), INVALID), (dict(rope_batch_stride=6), INVALID),
                                         (dict(seqlen_q=1 << 30, heads_q=4), UNSUPPORTED)])
 def test_bad_queries_are_refused(bad, status):
-    lib, c, q = bca.library(), ctypes.byref(cache()), ctypes.byref(query(**bad))
+    lib, c, q = bca.library(), cache(), query(**bad)
     assert lib.magi_bca_kv4_fwd(P, c, P, P, P, None, None, None, P, P, P, 1 << 40, q, None) == status
     assert lib.magi_bca_kv4_weights(P, c, P, P, P, P, None, P, 1.0, P, 1 << 40, q, None) == status
     for name in ("fwd", "weights"):
         f = getattr(lib, f"magi_bca_kv4_{name}_workspace_size")
-        assert f(ctypes.byref(cache()), ctypes.byref(query(**bad))) == 0
+        assert f(cache(), query(**bad)) == 0
 
 
 def test_append_and_read_arguments():
-    lib, c = bca.library(), ctypes.byref(cache())
-    ap = lambda k=P, v=P, start=P, n=1, stride=0, eps=1e-6: lib.magi_bca_kv4_append(  # noqa: E731
-        k, v, c, start, None, n, None, stride, eps, None)
+    lib, c = bca.library(), cache()
+    ap = lambda k=P, v=P, start=P, n=1, rope=None, stride=0, eps=1e-6: lib.magi_bca_kv4_append(  # noqa: E731
+        k, v, c, start, None, n, rope, stride, eps, None)
     assert ap(k=None) == ap(v=None) == ap(start=None) == ap(n=0) == ap(n=-3) == ap(stride=-1) == INVALID
+    assert ap(rope=P + 8) == ap(stride=2) == INVALID
     assert ap(k=P + 2) == ap(v=P + 8) == ap(eps=-1.0) == ap(eps=float("inf")) == INVALID
     rd = lambda k=P, v=P, n=1: lib.magi_bca_kv4_read(c, P, n, k, v, None)  # noqa: E731
     assert rd(k=None) == rd(v=None) == rd(n=0) == rd(k=P + 2) == INVALID
 
 
 def test_fwd_and_weights_arguments():
-    lib, c, q = bca.library(), ctypes.byref(cache()), ctypes.byref(query())
+    lib, c, q = bca.library(), cache(), query()
 
     def fwd(qp=P, ln=P, gq=P, gk=P, bo=None, bl=None, out=P, lse=P, ws=P, n=1 << 40, qq=q):
         return lib.magi_bca_kv4_fwd(qp, c, ln, gq, gk, None, bo, bl, out, lse, ws, n, qq, None)
@@ -126,7 +144,7 @@ def test_fwd_and_weights_arguments():
     assert fwd(bo=2 * P) == fwd(bl=2 * P) == INVALID                     # one without the other
     assert fwd(bo=P, bl=2 * P) == fwd(bo=2 * P, bl=P) == INVALID         # base in the outputs' place
     assert fwd(qp=P + 2) == fwd(out=P + 8) == fwd(bo=2 * P + 8, bl=2 * P) == INVALID
-    big = ctypes.byref(query(seqlen_q=512))
+    big = query(seqlen_q=512)
     need = lib.magi_bca_kv4_fwd_workspace_size(c, big)
     assert need > 0
     assert fwd(qq=big, n=need - 1) == TOO_SMALL
@@ -148,7 +166,7 @@ def test_evict_arguments():
 
     def ev(w=P, ln=P, keep=8, recent=4, dw=2 * P, dl=2 * P, ix=P, **dst):
         d = cache(**{**b, **dst})
-        return lib.magi_bca_kv4_evict(ctypes.byref(a), w, ln, keep, recent, ctypes.byref(d), dw, dl, ix, None)
+        return lib.magi_bca_kv4_evict(a, w, ln, keep, recent, d, dw, dl, ix, None)
 
     assert ev(w=None) == ev(ln=None) == ev(dw=None) == ev(dl=None) == ev(ix=None) == INVALID
     assert ev(keep=0) == ev(recent=-1) == ev(recent=9) == ev(keep=257) == INVALID
@@ -161,12 +179,12 @@ def test_workspace_sizes():
     # a single token over short histories needs none, over long ones pieces of
     # rows to join, far less than the cache; its weights need none
     for capacity, low, high in ((128, 0, 0), (1 << 17, 1, 1 << 21)):
-        c = ctypes.byref(cache(batch=1, heads_kv=8, capacity=capacity))
-        assert low <= lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(heads_q=24))) <= high
-        assert lib.magi_bca_kv4_weights_workspace_size(c, ctypes.byref(query(heads_q=24))) == 0
+        c = cache(batch=1, heads_kv=8, capacity=capacity)
+        assert low <= lib.magi_bca_kv4_fwd_workspace_size(c, query(heads_q=24)) <= high
+        assert lib.magi_bca_kv4_weights_workspace_size(c, query(heads_q=24)) == 0
     # a chunk: the expanded cache and queries at least
-    c = ctypes.byref(cache(batch=2, heads_kv=8, capacity=92160))
-    n = lib.magi_bca_kv4_fwd_workspace_size(c, ctypes.byref(query(seqlen_q=5760, heads_q=24)))
+    c = cache(batch=2, heads_kv=8, capacity=92160)
+    n = lib.magi_bca_kv4_fwd_workspace_size(c, query(seqlen_q=5760, heads_q=24))
     assert n >= 2 * 8 * 92160 * 128 * 2 * 2 + 2 * 24 * 5760 * 128 * 2
 
 
