@@ -100,5 +100,22 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
 
+// `all` steps in n parts, the first all % n of them a step longer.  No more
+// parts than get kLeast steps each.
+template <int kLeast>
+struct Parts {
+  int n, size, longer;
+  __device__ __forceinline__ Parts(int all, int ctas) {
+    n = min(ctas, (all + kLeast - 1) / kLeast);
+    size = n > 0 ? all / n : 0;
+    longer = all - n * size;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i >= n ? n * size + longer : i * size + min(i, longer); }
+  __device__ __forceinline__ int of(int x) const {   // the part that holds step x
+    const int head = longer * (size + 1);
+    return x < head ? x / (size + 1) : longer + (x - head) / size;
+  }
+};
+
 }  // namespace kv4
 }  // namespace magi

@@ -83,8 +83,8 @@ struct FwdParams4 {
   float* lse;                 // or nullptr
   int heads_q, sq;
   float scale_log2, eps;
-  int n_splits;            // chunk path: parts of a history that different CTAs read
-  float* part_o;           // rows of D fp32: chunk path [n_splits, B, H, G * Sq], token path [slot, row of a tile]
+  int n_splits;            // weights, chunk path: parts of the queries that different CTAs take
+  float* part_o;           // pieces to join: attention [slot, row of a tile, D]; weights [n_splits, B, H, cap]
   float2* part_ml;         // for each such row (reference in log2 units, sum)
   uint16_t* qh;            // chunk path: folded queries [B, H, G * Sq, D] fp16 (high part)
   uint16_t* ql;            //   and low part (weights only)
@@ -119,15 +119,14 @@ cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s);
 cudaError_t launch_token_weights(const FwdParams4& p, cudaStream_t s);
 
 // Many rows: expanded fp16 operands and the tensor cores of tcgen05.
-int chunk_splits(const Cache& c, int rows);
+int64_t chunk_piece_rows(const Cache& c, int rows);   // rows of the fwd's part_o / part_ml
+bool chunk_units_fit(const Cache& c, int rows);
 int chunk_weight_splits(const Cache& c, int rows_pad);
 cudaError_t launch_expand(const FwdParams4& p, bool values, bool low, cudaStream_t s);
 cudaError_t launch_chunk_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
                              cudaStream_t s);
 cudaError_t launch_chunk_weights(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk,
                                  const FwdParams4& p, cudaStream_t s);
-
-cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s);
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 

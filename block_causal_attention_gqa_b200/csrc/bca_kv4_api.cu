@@ -45,7 +45,8 @@ int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
   if (q->heads_q % c.heads_kv != 0) return MAGI_BCA_UNSUPPORTED;
   if ((int64_t)c.batch * q->heads_q * q->seqlen_q >= (int64_t(1) << 31)) return MAGI_BCA_UNSUPPORTED;
   const int rows = q->heads_q / c.heads_kv * q->seqlen_q;
-  if (rows <= kTokenWeightRows && !token_steps_fit(to_cache(c), rows)) return MAGI_BCA_UNSUPPORTED;
+  if (!token_steps_fit(to_cache(c), std::min(rows, kTokenWeightRows)) || !chunk_units_fit(to_cache(c), rows))
+    return MAGI_BCA_UNSUPPORTED;
   return MAGI_BCA_OK;
 }
 
@@ -70,31 +71,25 @@ Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weig
   };
   p.token = rows <= (weights ? kTokenWeightRows : kTokenFwdRows);
   p.rows_pad = (int)(((int64_t)rows + 127) / 128 * 128);
+  auto pieces = [&](int64_t n) {
+    p.part_o = take((size_t)n * D * 4);
+    p.part_ml = take((size_t)n * 8);
+  };
   if (p.token) {
-    if (!weights) {
-      const size_t n = (size_t)token_piece_rows(cc, rows);   // 0 for short histories
-      p.part_o = take(n * D * 4);
-      p.part_ml = take(n * 8);
-    }
-  } else {
-    p.splits = weights ? chunk_weight_splits(cc, p.rows_pad) : chunk_splits(cc, rows);
-    p.qh = take(BH * rows * D * 2);
-    p.kx = take(BH * c.capacity * D * 2);
-    if (weights) {
-      p.ql = take(BH * rows * D * 2);
-      p.neg_lse = take(BH * p.rows_pad * 4);
-    } else {
-      p.vx = take(BH * c.capacity * D * 2);
-      p.alpha = take(BH * rows * 4);
-    }
+    if (!weights) pieces(token_piece_rows(cc, rows));   // none for short histories
+    return p;
   }
-  if (!p.token && p.splits > 1) {
-    if (!weights) {
-      p.part_o = take((size_t)p.splits * BH * rows * D * 4);
-      p.part_ml = take((size_t)p.splits * BH * rows * 8);
-    } else {
-      p.part_o = take((size_t)p.splits * BH * c.capacity * 4);
-    }
+  p.qh = take(BH * rows * D * 2);
+  p.kx = take(BH * c.capacity * D * 2);
+  if (weights) {
+    p.splits = chunk_weight_splits(cc, p.rows_pad);
+    p.ql = take(BH * rows * D * 2);
+    p.neg_lse = take(BH * p.rows_pad * 4);
+    if (p.splits > 1) p.part_o = take((size_t)p.splits * BH * c.capacity * 4);
+  } else {
+    p.vx = take(BH * c.capacity * D * 2);
+    p.alpha = take(BH * rows * 4);
+    pieces(chunk_piece_rows(cc, rows));
   }
   return p;
 }
@@ -213,18 +208,15 @@ int magi_bca_kv4_fwd(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, co
   p.lse = lse;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (plan.token) return done("cache attention launch", launch_token_fwd(p, cs));
-  {
-    const int BH = cache->batch * cache->heads_kv, rows = rows_of(*cache, *query), D = cache->head_dim;
-    CUtensorMap tq, tk, tv;
-    if (make_tensor_map_bf16(&tq, p.qh, BH, rows, 1, D) != MAGI_BCA_OK ||
-        make_tensor_map_bf16(&tk, p.kx, BH, cache->capacity, 1, D) != MAGI_BCA_OK ||
-        make_tensor_map_bf16(&tv, p.vx, BH, cache->capacity, 1, D) != MAGI_BCA_OK)
-      return MAGI_BCA_CUDA_ERROR;
-    st = done("cache expansion launch", launch_expand(p, true, false, cs));
-    if (st == MAGI_BCA_OK) st = done("cache attention launch", launch_chunk_fwd(tq, tk, tv, p, cs));
-  }
-  if (st != MAGI_BCA_OK || plan.splits == 1) return st;
-  return done("cache attention combine launch", launch_combine(p, cs));
+  const int BH = cache->batch * cache->heads_kv, rows = rows_of(*cache, *query), D = cache->head_dim;
+  CUtensorMap tq, tk, tv;
+  if (make_tensor_map_bf16(&tq, p.qh, BH, rows, 1, D) != MAGI_BCA_OK ||
+      make_tensor_map_bf16(&tk, p.kx, BH, cache->capacity, 1, D) != MAGI_BCA_OK ||
+      make_tensor_map_bf16(&tv, p.vx, BH, cache->capacity, 1, D) != MAGI_BCA_OK)
+    return MAGI_BCA_CUDA_ERROR;
+  st = done("cache expansion launch", launch_expand(p, true, false, cs));
+  if (st != MAGI_BCA_OK) return st;
+  return done("cache attention launch", launch_chunk_fwd(tq, tk, tv, p, cs));
 }
 
 int magi_bca_kv4_weights(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, const int32_t* lengths,

@@ -15,8 +15,14 @@
 // runs two of them against the same key/value tiles, with the roles and the
 // softmax of the forward kernel (bca_fwd.cu): warps 0-3 and 4-7 a softmax
 // warpgroup each, warp 8 issues the products, warp 9 the copies.  P is fp16 and
-// carries 2^7, the reference moves when a score passes it by 8.  A history is
-// cut into n_splits parts when the row tiles alone leave SMs idle.
+// carries 2^7, the reference moves when a score passes it by 8.
+//   Split.  One CTA runs on an SM and takes unit after unit (a pair of row tiles
+// of one head).  As many rounds of whole units as all CTAs have (neighbours then
+// read the same keys at the same time), and the units that are left over cut
+// into equal parts; kv4_chunk_combine_kernel joins their pieces.  In whole units
+// alone 540 of them take 4 rounds of 148 where 3.65 would do (1508 us against
+// XX), and 64 leave most SMs idle.  The barriers' phases run on from unit to
+// unit, so the next unit's copies and first product overlap the last one's end.
 //
 // Weights (kv4_chunk_weights_kernel).  w_j sums over queries, so the tile is
 // turned: S^T = K^ Q^^T, a thread owns a key (a TMEM lane) and sums over the
@@ -43,7 +49,7 @@ constexpr float kMove = 8.f;
 constexpr float kLift = 7.f;
 
 enum : int {
-  kErrQ = 3111, kErrKFull, kErrVFull, kErrKEmpty, kErrVEmpty, kErrSFull, kErrPReady,
+  kErrQ = 3111, kErrKFull, kErrVFull, kErrKEmpty, kErrVEmpty, kErrSFull, kErrPReady, kErrQEmpty,
   kErrWK = 3121, kErrWQFull, kErrWQEmpty, kErrWSFull, kErrWSEmpty, kErrWLse
 };
 
@@ -73,7 +79,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool o
 // to a tile of 128 (zeros there), in items of one key block (16 features of a
 // token) or one value block (8 features of two tokens).
 template <int D, bool kValues, bool kLow>
-__global__ void __launch_bounds__(256) kv4_expand_kernel(const FwdParams4 p, int fold_blocks) {
+__global__ void __launch_bounds__(256, 3) kv4_expand_kernel(const FwdParams4 p, int fold_blocks) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
   const int BH = p.c.batch * p.c.heads;
@@ -145,38 +152,50 @@ __global__ void __launch_bounds__(256) kv4_expand_kernel(const FwdParams4 p, int
     }
     return;
   }
-  constexpr int kPerTile = 128 * (D / 16);               // key blocks of a tile; as many value blocks
-  const int tiles = (p.c.cap + 127) / 128;
+  const int tiles = p.c.cap / 128;
   const int64_t items = (int64_t)BH * tiles;
   for (int64_t it = (int64_t)blockIdx.x - fold_blocks; it < items; it += (int64_t)gridDim.x - fold_blocks) {
     const int bh = (int)(it / tiles), tile = (int)(it % tiles);
     const int len = min(max(__ldg(p.lengths + bh / p.c.heads), 0), p.c.cap);
     if (tile * 128 >= len) continue;
     const int64_t tok0 = (int64_t)bh * p.c.cap + tile * 128;
-    for (int i = threadIdx.x; i < kPerTile; i += 256) {
-      const int t = i / (D / 16), blk = i % (D / 16);
-      uint2 w = __ldg(reinterpret_cast<const uint2*>(p.c.kc + tok0 * (D / 2)) + i);
-      uint32_t s = scale_dup(__ldg(p.c.ks + tok0 * (D / 16) + i));
-      if (tile * 128 + t >= len) { w = make_uint2(0, 0); s = 0; }
+    // a thread's key and value blocks of the tile, all loads before the first store
+    constexpr int kN = 128 * (D / 16) / 256;
+    uint2 kw[kN], vw[kN];
+    uint32_t ks[kN], vs[kN];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int i = n * 256 + threadIdx.x;
+      kw[n] = __ldg(reinterpret_cast<const uint2*>(p.c.kc + tok0 * (D / 2)) + i);
+      ks[n] = __ldg(p.c.ks + tok0 * (D / 16) + i);
+      if constexpr (kValues) {
+        const int pr = i / (D / 8), f = i % (D / 8) * 8;   // row of two tokens, first of 8 features
+        vw[n] = __ldg(reinterpret_cast<const uint2*>(p.c.vc + (tok0 / 2 + pr) * D + f));
+        vs[n] = __ldg(reinterpret_cast<const uint16_t*>(p.c.vs + ((tok0 / 2 + pr) * (D / 16) + f / 16) * 2));
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int i = n * 256 + threadIdx.x, t = i / (D / 16), blk = i % (D / 16);
+      const bool behind = tile * 128 + t >= len;
+      const uint32_t s = behind ? 0u : scale_dup(ks[n]);
       uint32_t a[4], c[4];
-      codes_f16x8(w.x, a);
-      codes_f16x8(w.y, c);
+      codes_f16x8(behind ? 0u : kw[n].x, a);
+      codes_f16x8(behind ? 0u : kw[n].y, c);
       uint4* dst = reinterpret_cast<uint4*>(p.kx + (tok0 + t) * D + blk * 16);
       dst[0] = make_uint4(hmul2(a[0], s), hmul2(a[1], s), hmul2(a[2], s), hmul2(a[3], s));
       dst[1] = make_uint4(hmul2(c[0], s), hmul2(c[1], s), hmul2(c[2], s), hmul2(c[3], s));
     }
     if constexpr (kValues) {
-      for (int i = threadIdx.x; i < 64 * (D / 8); i += 256) {
-        const int pr = i / (D / 8), f = i % (D / 8) * 8;   // row of two tokens, first of 8 features
-        const int64_t vrow = tok0 / 2 + pr;
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.c.vc + vrow * D + f));
-        const uint32_t s2 = __ldg(reinterpret_cast<const uint16_t*>(p.c.vs + (vrow * (D / 16) + f / 16) * 2));
-        uint32_t s = scale_pair(s2);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const int i = n * 256 + threadIdx.x, pr = i / (D / 8), f = i % (D / 8) * 8;
         const int t = tile * 128 + 2 * pr;
+        uint32_t s = scale_pair(vs[n]);
         if (t + 1 >= len) s = t >= len ? 0u : s & 0xffffu;
         uint32_t a[8];
-        codes_f16x8(w.x, reinterpret_cast<uint32_t(&)[4]>(a[0]));
-        codes_f16x8(w.y, reinterpret_cast<uint32_t(&)[4]>(a[4]));
+        codes_f16x8(vw[n].x, reinterpret_cast<uint32_t(&)[4]>(a[0]));
+        codes_f16x8(vw[n].y, reinterpret_cast<uint32_t(&)[4]>(a[4]));
         uint32_t even[4], odd[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -200,21 +219,101 @@ struct FwdLayout {
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  static constexpr int kTmemSlot = kBars + 16 * 8;
-  static constexpr int kAlloc = kTmemSlot + 16 + 1024;   // slack for 1024-byte alignment
+  static constexpr int kTmemSlot = kBars + 18 * 8;
+  static constexpr int kPart = kTmemSlot + 16;
+  static constexpr int kWalk = kPart + 16;               // a walk and its piece for each softmax warpgroup
+  static constexpr int kAlloc = kWalk + 2 * 96 + 1024;   // slack for 1024-byte alignment
 };
 
 struct FwdBars {
-  uint64_t q_full[2], s_full[2], p_ready[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
 };
 
+// ---- units: pairs of row tiles, numbered by batch element, head and pair
+__device__ __forceinline__ int tiles_of(const FwdParams4& p, int b) {
+  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  return (len + 127) / 128;
+}
+
+// Tiles of the units from u0 on that belong to batch elements below b, and of
+// all of them, by one warp.  per: units of a batch element.
+__device__ __forceinline__ void tiles_below(const FwdParams4& p, int u0, int per, int b, int lane, int& below, int& all) {
+  const int b0 = u0 / per;
+  below = all = 0;
+  for (int i = b0 + lane; i < p.c.batch; i += 32) {
+    const int t = tiles_of(p, i) * (i == b0 ? per - (u0 - b0 * per) : per);
+    all += t;
+    if (i < b) below += t;
+  }
+  below = __reduce_add_sync(0xffffffffu, below);
+  all = __reduce_add_sync(0xffffffffu, all);
+}
+
+// What a CTA does, piece after piece.  Every role walks the same pieces.
+struct Walk {
+  int per, pairs, rounds, u0;   // whole units first, then [x, x1) of the tiles of the units from u0 on
+  int round = 0;
+  int x, x1;
+  int u, begin;                 // a unit and the flat tile it begins at, at or before x
+};
+
+struct Piece {
+  int b, hk, bh, m0, len, t_begin, n_vis, slot;
+  int whole, more;
+};
+
+// The softmax warpgroups' walk is kept by one thread and read from shared
+// memory: their registers are full.
+struct SharedWalk {
+  Walk walk;
+  Piece piece;
+};
+static_assert(sizeof(SharedWalk) <= 96, "FwdLayout::kWalk");
+
+__device__ __forceinline__ bool next_piece(const FwdParams4& p, Walk& w, Piece& o) {
+  int u, tiles;
+  for (;;) {
+    if (w.round < w.rounds) {
+      u = (int)blockIdx.x + w.round * (int)gridDim.x;
+      ++w.round;
+      o.b = u / w.per;
+      o.len = min(max(__ldg(p.lengths + o.b), 0), p.c.cap);
+      tiles = (o.len + 127) / 128;
+      if (tiles == 0) continue;
+      o.t_begin = 0;
+      o.n_vis = tiles;
+      break;
+    }
+    if (w.x >= w.x1) return false;
+    u = w.u;
+    o.b = u / w.per;
+    o.len = min(max(__ldg(p.lengths + o.b), 0), p.c.cap);
+    tiles = (o.len + 127) / 128;
+    if (w.x >= w.begin + tiles) {   // past this unit
+      w.begin += tiles;
+      ++w.u;
+      continue;
+    }
+    o.t_begin = w.x - w.begin;
+    o.n_vis = min(tiles - o.t_begin, w.x1 - w.x);
+    w.x += o.n_vis;
+    break;
+  }
+  const int rem = u - o.b * w.per;
+  o.hk = rem / w.pairs;
+  o.m0 = (rem - o.hk * w.pairs) * 256;
+  o.bh = o.b * p.c.heads + o.hk;
+  o.whole = o.t_begin == 0 && o.n_vis == tiles;
+  o.slot = (int)blockIdx.x + u - w.u0;
+  return true;
+}
+
 template <int D>
-__device__ __forceinline__ void write_part(const FwdParams4& p, int split, int bh, int rows, int row, int f0, float m,
-                                           float l, const float (&o)[32]) {
-  const int64_t at = ((int64_t)split * p.c.batch * p.c.heads + bh) * rows + row;
+__device__ __forceinline__ void write_piece(const FwdParams4& p, int slot, int row, int f0, float m, float l,
+                                            const float (&o)[32]) {
+  const int64_t at = (int64_t)slot * 256 + row;
   if (f0 == 0) p.part_ml[at] = make_float2(m, l);
-  if (m == -INFINITY) return;
 #pragma unroll
   for (int f = 0; f < 32; f += 4)
     *reinterpret_cast<float4*>(p.part_o + at * D + f0 + f) = make_float4(o[f], o[f + 1], o[f + 2], o[f + 3]);
@@ -229,34 +328,33 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FwdBars* bars = reinterpret_cast<FwdBars*>(smem + L::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  int4* part = reinterpret_cast<int4*>(smem + L::kPart);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = (int)gridDim.x / p.n_splits;
-  const int split = blockIdx.x / pairs, pair = blockIdx.x % pairs, bh = blockIdx.y;
-  const int b = bh / p.c.heads, hk = bh % p.c.heads;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
-  const int m0 = pair * 256;
-  const int n_sub = m0 + 128 < rows ? 2 : 1;
-  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
-  const int tiles = (len + 127) / 128;
-  const int t_begin = (int)((int64_t)tiles * split / p.n_splits);
-  const int n_vis = (int)((int64_t)tiles * (split + 1) / p.n_splits) - t_begin;
-  if (n_vis == 0) {   // nothing to see: the rows are the base part's, or empty
+  Walk walk;
+  walk.pairs = (rows + 255) / 256;
+  walk.per = p.c.heads * walk.pairs;
+  walk.rounds = p.c.batch * walk.per / (int)gridDim.x;
+  walk.u0 = walk.rounds * (int)gridDim.x;
+
+  // batch elements without a key: their rows are the base part's, or empty
+  for (int b = 0; b < p.c.batch; ++b) {
+    if (tiles_of(p, b) > 0) continue;
     float zero[32] = {};
-    const int row = m0 + threadIdx.x;
-    if (threadIdx.x < 256 && row < rows) {
-      for (int f = 0; f < D; f += 32) {
-        if (p.n_splits > 1) write_part<D>(p, split, bh, rows, row, f, -INFINITY, 0.f, zero);
-        else finish_row<32>(p, b, hk, G, row, D, f, -INFINITY, 0.f, zero);
-      }
+    for (int u = blockIdx.x; u < walk.per; u += gridDim.x) {
+      const int row = u % walk.pairs * 256 + threadIdx.x;
+      if (threadIdx.x < 256 && row < rows)
+        for (int f = 0; f < D; f += 32) finish_row<32>(p, b, u / walk.pairs, G, row, D, f, -INFINITY, 0.f, zero);
     }
-    return;
   }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 1);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_ready[s], 1);
+      mbar_init(&bars->o_full[s], 1);
     }
     for (int st = 0; st < kStages; ++st) {
       mbar_init(&bars->k_full[st], 1);
@@ -275,38 +373,77 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  if (warp == 0) {   // this CTA's part of the units left over
+    int none, all = 0;
+    if (walk.u0 < p.c.batch * walk.per) tiles_below(p, walk.u0, walk.per, 0, lane, none, all);
+    const Parts<4> parts(all, (int)gridDim.x);
+    const int x0 = parts.begin(blockIdx.x), x1 = parts.begin(blockIdx.x + 1);
+    // the unit x0 lies in: batch element by batch element
+    int u = walk.u0, begin = 0;
+    while (x0 < x1) {
+      const int b = u / walk.per, t = tiles_of(p, b), n = (b + 1) * walk.per - u;
+      if (x0 < begin + t * n) {
+        const int k = (x0 - begin) / t;
+        u += k;
+        begin += k * t;
+        break;
+      }
+      begin += t * n;
+      u += n;
+    }
+    if (lane == 0) *part = make_int4(x0, x1, u, begin);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the expansion
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  walk.x = part->x;
+  walk.x1 = part->y;
+  walk.u = part->z;
+  walk.begin = part->w;
 
   if (warp == 9) {
+    // ------------------------------------------------------------ copies
     if (elect_one()) {
-      for (int s = 0; s < n_sub; ++s) {
-        mbar_arrive_expect_tx(&bars->q_full[s], L::kTile);
-        for (int box = 0; box < D / 64; ++box)
-          tma_load_4d(smem + L::kQ + s * L::kTile + box * 16384, &tm_q, &bars->q_full[s], box * 64, 0, m0 + s * 128, bh);
-      }
-      for (int j = 0; j < n_vis; ++j) {
-        const int st = j % kStages;
-        const uint32_t par = ((j / kStages) & 1) ^ 1;
-        if (!mbar_wait(&bars->k_empty[st], par, p.status, kErrKEmpty)) break;
-        mbar_arrive_expect_tx(&bars->k_full[st], L::kTile);
-        for (int box = 0; box < D / 64; ++box)
-          tma_load_4d(smem + L::kK + st * L::kTile + box * 16384, &tm_k, &bars->k_full[st], box * 64, 0,
-                      (t_begin + j) * 128, bh);
-        if (!mbar_wait(&bars->v_empty[st], par, p.status, kErrVEmpty)) break;
-        mbar_arrive_expect_tx(&bars->v_full[st], L::kTile);
-        for (int box = 0; box < D / 64; ++box)
-          tma_load_4d(smem + L::kV + st * L::kTile + box * 16384, &tm_v, &bars->v_full[st], box * 64, 0,
-                      (t_begin + j) * 128, bh);
+      Piece pc;
+      uint32_t kv = 0, nq[2] = {0, 0};   // tiles and queries so far
+      bool ok = true;
+      while (ok && next_piece(p, walk, pc)) {
+        const int n_sub = pc.m0 + 128 < rows ? 2 : 1;
+        for (int s = 0; s < n_sub && ok; ++s) {
+          ok = mbar_wait(&bars->q_empty[s], (nq[s]++ & 1) ^ 1, p.status, kErrQEmpty);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars->q_full[s], L::kTile);
+          for (int box = 0; box < D / 64; ++box)
+            tma_load_4d(smem + L::kQ + s * L::kTile + box * 16384, &tm_q, &bars->q_full[s], box * 64, 0,
+                        pc.m0 + s * 128, pc.bh);
+        }
+        for (int j = 0; j < pc.n_vis && ok; ++j, ++kv) {
+          const uint32_t st = kv % kStages, par = ((kv / kStages) & 1) ^ 1;
+          const int tok = (pc.t_begin + j) * 128;
+          ok = mbar_wait(&bars->k_empty[st], par, p.status, kErrKEmpty);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars->k_full[st], L::kTile);
+          for (int box = 0; box < D / 64; ++box)
+            tma_load_4d(smem + L::kK + st * L::kTile + box * 16384, &tm_k, &bars->k_full[st], box * 64, 0, tok, pc.bh);
+          ok = mbar_wait(&bars->v_empty[st], par, p.status, kErrVEmpty);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars->v_full[st], L::kTile);
+          for (int box = 0; box < D / 64; ++box)
+            tma_load_4d(smem + L::kV + st * L::kTile + box * 16384, &tm_v, &bars->v_full[st], box * 64, 0, tok, pc.bh);
+        }
       }
     }
   } else if (warp == 8) {
+    // ---------------------------------------------------------- products
     if (elect_one()) {
+      Piece pc;
       constexpr uint32_t idesc_s = make_idesc_f16(128, 128, false);
       constexpr uint32_t idesc_o = make_idesc_f16(128, D, true);
       const uint32_t q_base = smem_u32(smem + L::kQ), k_base = smem_u32(smem + L::kK), v_base = smem_u32(smem + L::kV);
+      uint32_t kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
       bool ok = true;
       auto issue_s = [&](int s, int st) {
         const uint32_t qa = q_base + s * L::kTile, ka = k_base + st * L::kTile;
@@ -317,57 +454,77 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                       idesc_s, kk > 0);
         }
       };
-      for (int s = 0; s < n_sub && ok; ++s) ok = mbar_wait(&bars->q_full[s], 0, p.status, kErrQ);
-      ok = ok && mbar_wait(&bars->k_full[0], 0, p.status, kErrKFull);
-      if (ok) {
+      while (ok && next_piece(p, walk, pc)) {
+        const int n_sub = pc.m0 + 128 < rows ? 2 : 1;
+        for (int s = 0; s < n_sub && ok; ++s) ok = mbar_wait(&bars->q_full[s], nq[s]++ & 1, p.status, kErrQ);
+        ok = ok && mbar_wait(&bars->k_full[kv % kStages], (kv / kStages) & 1, p.status, kErrKFull);
+        if (!ok) break;
         tc_fence_after();
         for (int s = 0; s < n_sub; ++s) {
-          issue_s(s, 0);
+          issue_s(s, kv % kStages);
           mma_commit(&bars->s_full[s]);
+          if (pc.n_vis == 1) mma_commit(&bars->q_empty[s]);
         }
-        mma_commit(&bars->k_empty[0]);
-      }
-      for (int j = 0; j < n_vis && ok; ++j) {
-        const int st = j % kStages;
-        if (!mbar_wait(&bars->v_full[st], (j / kStages) & 1, p.status, kErrVFull)) break;
-        const bool has_next = j + 1 < n_vis;
-        const int st1 = (j + 1) % kStages;
-        for (int s = 0; s < n_sub; ++s) {
-          if (!mbar_wait(&bars->p_ready[s], j & 1, p.status, kErrPReady)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t va = v_base + st * L::kTile;
+        mma_commit(&bars->k_empty[kv % kStages]);
+        for (int j = 0; j < pc.n_vis && ok; ++j, ++kv) {
+          const uint32_t st = kv % kStages, st1 = (kv + 1) % kStages;
+          ok = mbar_wait(&bars->v_full[st], (kv / kStages) & 1, p.status, kErrVFull);
+          if (!ok) break;
+          const bool has_next = j + 1 < pc.n_vis;
+          for (int s = 0; s < n_sub; ++s) {
+            ok = mbar_wait(&bars->p_ready[s], np[s]++ & 1, p.status, kErrPReady);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t va = v_base + st * L::kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + 256 * s + 128, tmem + 256 * s + kk * 8, make_sw128_desc(va + kk * 2048, 16384, 1024),
-                        idesc_o, j > 0 || kk > 0);
-          if (has_next) {
-            if (s == 0 && !mbar_wait(&bars->k_full[st1], ((j + 1) / kStages) & 1, p.status, kErrKFull)) {
-              ok = false;
-              break;
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tmem + 256 * s + 128, tmem + 256 * s + kk * 8, make_sw128_desc(va + kk * 2048, 16384, 1024),
+                          idesc_o, j > 0 || kk > 0);
+            if (has_next) {
+              if (s == 0) {
+                ok = mbar_wait(&bars->k_full[st1], ((kv + 1) / kStages) & 1, p.status, kErrKFull);
+                if (!ok) break;
+              }
+              issue_s(s, st1);
+              mma_commit(&bars->s_full[s]);
+              if (j + 2 == pc.n_vis) mma_commit(&bars->q_empty[s]);
+            } else {
+              mma_commit(&bars->o_full[s]);
             }
-            issue_s(s, st1);
           }
-          mma_commit(&bars->s_full[s]);
+          if (!ok) break;
+          mma_commit(&bars->v_empty[st]);
+          if (has_next) mma_commit(&bars->k_empty[st1]);
         }
-        if (!ok) break;
-        mma_commit(&bars->v_empty[st]);
-        if (has_next) mma_commit(&bars->k_empty[st1]);
       }
     }
   } else {
+    // ----------------------------------------------------------- softmax
     const int s = warp >> 2, r = threadIdx.x & 127;
-    if (s < n_sub) {
-      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t t_s = tmem + lane_base + 256 * s;
-      const uint32_t t_o = tmem + lane_base + 256 * s + 128;
-      const int bar_id = 1 + s;
-      const int row = m0 + s * 128 + r;
-      bool ok = true;
-      const float scale = row < rows ? p.alpha[(int64_t)bh * rows + row] : 1.f;   // of the row's scores
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + 256 * s;
+    const uint32_t t_o = tmem + lane_base + 256 * s + 128;
+    const int bar_id = 1 + s;
+    uint32_t ns = 0, no = 0;
+    bool ok = true;
+    SharedWalk* sw = reinterpret_cast<SharedWalk*>(smem + L::kWalk + s * 96);
+    if (r == 0) sw->walk = walk;
+    const volatile Piece* pc = &sw->piece;
+    for (;;) {
+      if (r == 0) sw->piece.more = next_piece(p, sw->walk, sw->piece);
+      named_bar_sync(bar_id, 128);
+      if (!pc->more) break;
+      const int row = pc->m0 + s * 128 + r, n_vis = pc->n_vis;
+      const int lim0 = pc->len - pc->t_begin * 128;   // keys of the history from the piece's first tile on
+      if (pc->m0 + s * 128 >= rows) {                 // a single row tile
+        named_bar_sync(bar_id, 128);
+        continue;
+      }
+      const float scale = row < rows ? p.alpha[(int64_t)pc->bh * rows + row] : 1.f;   // of the row's scores
       const uint64_t scale2 = f2_pack(scale, scale);
       float m_ref = -INFINITY, l_sum = 0.f;
       for (int j = 0; j < n_vis; ++j) {
-        ok = warp_wait(&bars->s_full[s], j & 1, ok, p.status, kErrSFull);
+        ok = warp_wait(&bars->s_full[s], ns++ & 1, ok, p.status, kErrSFull);
         if (ok) {
           tc_fence_after();
           uint64_t x2[64];
@@ -382,7 +539,7 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               for (int i = 0; i < 16; ++i)
                 x2[c * 16 + i] = f2_pack(__uint_as_float(raw[c][2 * i]), __uint_as_float(raw[c][2 * i + 1]));
           }
-          const int lim = len - (t_begin + j) * 128;
+          const int lim = lim0 - j * 128;
           const bool masked = lim < 128;   // the last tile only
           if (masked) {
 #pragma unroll
@@ -471,7 +628,7 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         named_bar_sync(bar_id, 128);
         if (r == 0 && ok) mbar_arrive(&bars->p_ready[s]);
       }
-      ok = warp_wait(&bars->s_full[s], n_vis & 1, ok, p.status, kErrSFull);
+      ok = warp_wait(&bars->o_full[s], no++ & 1, ok, p.status, kErrSFull);
       if (ok) {
         tc_fence_after();
         // scores that are NaN (a query that is) leave the reference at -inf: it
@@ -485,12 +642,11 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           float o[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
-          if (row < rows) {
-            if (p.n_splits > 1) write_part<D>(p, split, bh, rows, row, c * 32, m, l_sum, o);
-            else finish_row<32>(p, b, hk, G, row, D, c * 32, m, l_sum, o);
-          }
+          if (!pc->whole) write_piece<D>(p, pc->slot, s * 128 + r, c * 32, m, l_sum, o);
+          else if (row < rows) finish_row<32>(p, pc->b, pc->hk, G, row, D, c * 32, m, l_sum, o);
         }
       }
+      named_bar_sync(bar_id, 128);   // the piece has been read
     }
   }
   tc_fence_before();
@@ -501,36 +657,56 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
-// Joins the parts of the rows: one warp a row.
+// Joins the pieces of the units from u0 on that were cut: a warp takes four
+// rows, whose loads are under way together.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const FwdParams4 p) {
-  constexpr int F = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(256) kv4_chunk_combine_kernel(const FwdParams4 p, int u0, int ctas) {
+  constexpr int F = D / 32, kR = 4;
   const int lane = threadIdx.x & 31;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
-  const int64_t groups = (int64_t)p.c.batch * p.c.heads;
-  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= groups * rows) return;
-  const int64_t stride = groups * rows;
-  float mm = -INFINITY;
-  for (int s = lane; s < p.n_splits; s += 32) mm = fmaxf(mm, p.part_ml[s * stride + r].x);
+  const int pairs = (rows + 255) / 256, per = p.c.heads * pairs;
+  const int u = u0 + (int)blockIdx.y, b = u / per, rem = u - b * per, hk = rem / pairs;
+  const int r = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * kR, row = (rem - hk * pairs) * 256 + r;
+  int below, all;
+  tiles_below(p, u0, per, b, lane, below, all);
+  const int tiles = tiles_of(p, b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= rows || tiles == 0) return;   // no keys: finished where that was seen
+  const Parts<4> parts(all, ctas);
+  const int x0 = below + (u - max(u0, b * per)) * tiles;
+  const int c0 = parts.of(x0), n = parts.of(x0 + tiles - 1) - c0 + 1;
+  if (n == 1) return;                      // not cut
+  const int64_t at0 = (int64_t)(c0 + u - u0) * 256 + r;   // piece i: 256 rows on
+  float mm[kR], ll[kR], acc[kR][F];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  float acc[F] = {}, ll = 0.f;
-  if (mm != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < p.n_splits; ++s) {
-      const int64_t at = s * stride + r;
-      const float2 ml = p.part_ml[at];
-      if (ml.x == -INFINITY) continue;     // an empty part wrote no O
-      const float w = fast_exp2(ml.x - mm);
-      ll += ml.y * w;
+  for (int k = 0; k < kR; ++k) {
+    const float2 ml = p.part_ml[at0 + k];
+    mm[k] = ml.x;
+    ll[k] = ml.y;
+    load_floats<F>(p.part_o + (at0 + k) * D + lane * F, acc[k]);
+  }
+  for (int i = 1; i < n; ++i) {
+    float2 ml[kR];
+    float o[kR][F];
 #pragma unroll
-      for (int f = 0; f < F; ++f) acc[f] = fmaf(p.part_o[at * D + lane * F + f], w, acc[f]);
+    for (int k = 0; k < kR; ++k) {
+      const int64_t at = at0 + (int64_t)i * 256 + k;
+      ml[k] = p.part_ml[at];
+      load_floats<F>(p.part_o + at * D + lane * F, o[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {         // every piece has a key, so the references are finite
+      const float m1 = fmaxf(mm[k], ml[k].x);
+      const float w0 = fast_exp2(mm[k] - m1), w1 = fast_exp2(ml[k].x - m1);
+      mm[k] = m1;
+      ll[k] = fmaf(ml[k].y, w1, ll[k] * w0);
+#pragma unroll
+      for (int f = 0; f < F; ++f) acc[k][f] = fmaf(o[k][f], w1, acc[k][f] * w0);
     }
   }
-  const int bh = (int)(r / rows);
-  finish_row<F>(p, bh / p.c.heads, bh % p.c.heads, G, (int)(r % rows), D, lane * F, mm, ll, acc);
+#pragma unroll
+  for (int k = 0; k < kR; ++k)
+    if (row + k < rows) finish_row<F>(p, b, hk, G, row + k, D, lane * F, mm[k], ll[k], acc[k]);
 }
 
 // ------------------------------------------------------------------ weights
@@ -563,7 +739,10 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
   const int tile = blockIdx.x, bh = blockIdx.y, split = blockIdx.z;
   const int b = bh / p.c.heads;
   const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
-  if (tile * 128 >= len) return;
+  if (tile * 128 >= len) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int q_tiles = p.rows_pad / 128;
   const int q_begin = (int)((int64_t)q_tiles * split / p.n_splits);
   const int n = (int)((int64_t)q_tiles * (split + 1) / p.n_splits) - q_begin;   // >= 1: n_splits <= q_tiles
@@ -594,6 +773,7 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the expansion
 
   if (warp == 9) {
     if (elect_one()) {
@@ -708,6 +888,30 @@ __global__ void __launch_bounds__(256) kv4_weights_sum_kernel(const FwdParams4 p
   p.weights[i] = p.decay != 0.f ? fmaf(p.decay, p.weights[i], x) : x;
 }
 
+// A launch that may start while the kernel before it is ending (the kernels wait
+// for it themselves).
+template <typename... Args>
+cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int block, int smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Units of the attention, and the CTAs that take them: one an SM, fewer only if
+// full caches would not give each 4 tiles.
+int chunk_units(const Cache& c, int rows) { return c.batch * c.heads * ((rows + 255) / 256); }
+int chunk_ctas(const Cache& c, int rows) {
+  return (int)std::min<int64_t>(148, std::max<int64_t>(1, (int64_t)chunk_units(c, rows) * (c.cap / 128) / 4));
+}
+
 template <int D>
 cudaError_t expand_d(const FwdParams4& p, bool values, bool low, cudaStream_t s) {
   const int64_t items = (int64_t)p.c.batch * p.c.heads * p.sq;
@@ -723,12 +927,14 @@ template <int D>
 cudaError_t chunk_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
                         cudaStream_t s) {
   static SmemRecord have;
-  const cudaError_t e = allow_smem(kv4_chunk_fwd_kernel<D>, FwdLayout<D>::kAlloc, have);
+  cudaError_t e = allow_smem(kv4_chunk_fwd_kernel<D>, FwdLayout<D>::kAlloc, have);
   if (e != cudaSuccess) return e;
   const int rows = p.heads_q / p.c.heads * p.sq;
-  const dim3 grid((rows + 255) / 256 * p.n_splits, p.c.batch * p.c.heads);
-  kv4_chunk_fwd_kernel<D><<<grid, kThreads, FwdLayout<D>::kAlloc, s>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  const int units = chunk_units(p.c, rows), ctas = chunk_ctas(p.c, rows);
+  e = launch_early(kv4_chunk_fwd_kernel<D>, dim3(ctas), kThreads, FwdLayout<D>::kAlloc, s, tq, tk, tv, p);
+  const int u0 = units / ctas * ctas;
+  if (e != cudaSuccess || u0 == units) return e;
+  return launch_early(kv4_chunk_combine_kernel<D>, dim3(8, units - u0), 256, 0, s, p, u0, ctas);
 }
 
 template <int D>
@@ -738,8 +944,8 @@ cudaError_t chunk_weights_d(const CUtensorMap& tqh, const CUtensorMap& tql, cons
   cudaError_t e = allow_smem(kv4_chunk_weights_kernel<D>, WLayout<D>::kAlloc, have);
   if (e != cudaSuccess) return e;
   const int BH = p.c.batch * p.c.heads;
-  kv4_chunk_weights_kernel<D><<<dim3(p.c.cap / 128, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s>>>(tqh, tql, tk, p);
-  e = cudaGetLastError();
+  e = launch_early(kv4_chunk_weights_kernel<D>, dim3(p.c.cap / 128, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s, tqh,
+                   tql, tk, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
   kv4_weights_sum_kernel<<<dim3((p.c.cap + 255) / 256, BH), 256, 0, s>>>(p);
   return cudaGetLastError();
@@ -747,12 +953,16 @@ cudaError_t chunk_weights_d(const CUtensorMap& tqh, const CUtensorMap& tql, cons
 
 }  // namespace
 
-// Parts of the history: a CTA takes 256 rows, one CTA runs on an SM.  Parts
-// are added while they fill more SMs, down to 4 tiles of a full cache each.
-int chunk_splits(const Cache& c, int rows) {
+// Rows of the attention's pieces: a slot of 256 for each CTA and unit that may be cut.
+int64_t chunk_piece_rows(const Cache& c, int rows) {
+  const int units = chunk_units(c, rows), ctas = chunk_ctas(c, rows), rest = units % ctas;
+  return rest == 0 ? 0 : (int64_t)(ctas + rest) * 256;
+}
+
+// Whether 32-bit numbers can count the units, and the tiles of those that may be cut.
+bool chunk_units_fit(const Cache& c, int rows) {
   const int64_t units = (int64_t)c.batch * c.heads * ((rows + 255) / 256);
-  const int64_t want = std::max<int64_t>(1, 148 / units);
-  return (int)std::min<int64_t>({want, std::max<int64_t>(1, c.cap / 512), (int64_t)32});
+  return units < (int64_t(1) << 30) && (int64_t)c.cap / 128 * 148 < (int64_t(1) << 31);
 }
 
 // Parts of the queries, for the weights: a CTA takes a key tile.
@@ -769,21 +979,6 @@ cudaError_t launch_expand(const FwdParams4& p, bool values, bool low, cudaStream
 cudaError_t launch_chunk_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams4& p,
                              cudaStream_t s) {
   return p.c.dim == 128 ? chunk_fwd_d<128>(tq, tk, tv, p, s) : chunk_fwd_d<64>(tq, tk, tv, p, s);
-}
-
-cudaError_t launch_combine(const FwdParams4& p, cudaStream_t s) {
-  const int64_t rows = (int64_t)p.c.batch * p.heads_q * p.sq;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return p.c.dim == 128 ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<128>, p)
-                        : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<64>, p);
 }
 
 cudaError_t launch_chunk_weights(const CUtensorMap& tqh, const CUtensorMap& tql, const CUtensorMap& tk,

@@ -184,28 +184,12 @@ __device__ __forceinline__ void steps_below(const FwdParams4& p, int b, int lane
   all = __reduce_add_sync(0xffffffffu, all);
 }
 
-// `all` steps in n parts, the first all % n of them a step longer.  No more
-// parts than have a step for each warp.
-struct Parts {
-  int n, size, longer;
-  __device__ __forceinline__ Parts(int all, int ctas) {
-    n = min(ctas, (all + kWarps - 1) / kWarps);
-    size = n > 0 ? all / n : 0;
-    longer = all - n * size;
-  }
-  __device__ __forceinline__ int begin(int i) const { return i >= n ? n * size + longer : i * size + min(i, longer); }
-  __device__ __forceinline__ int of(int x) const {   // the part that holds step x
-    const int head = longer * (size + 1);
-    return x < head ? x / (size + 1) : longer + (x - head) / size;
-  }
-};
-
 // This CTA's part [x0, x1), the batch element x0 lies in and the flat step that
 // begins at, by one warp.  per: histories of a batch element.
 __device__ __forceinline__ int4 find_part(const FwdParams4& p, int per, int lane) {
   int none, all;
   steps_below(p, 0, lane, none, all);
-  const Parts parts(all * per, (int)gridDim.x);
+  const Parts<kWarps> parts(all * per, (int)gridDim.x);
   const int x0 = parts.begin(blockIdx.x), x1 = parts.begin(blockIdx.x + 1);
   int begin = 0;
   for (int i0 = 0; x0 < x1 && i0 < p.c.batch; i0 += 32) {
@@ -532,7 +516,7 @@ __global__ void __launch_bounds__(256) kv4_token_combine_kernel(const FwdParams4
   int n = 0;
   int64_t slot = 0;
   if (steps > 0) {   // the parts that hold a step of the history
-    const Parts parts(all * per, ctas);
+    const Parts<kWarps> parts(all * per, ctas);
     const int x0 = below * per + hist * steps, c0 = parts.of(x0);
     slot = ((int64_t)b * per + hist + c0) * kRows + row % kRows;
     n = parts.of(x0 + steps - 1) - c0 + 1;
