@@ -27,9 +27,13 @@
 // Weights (kv4_chunk_weights_kernel).  w_j sums over queries, so the tile is
 // turned: S^T = K^ Q^^T, a thread owns a key (a TMEM lane) and sums over the
 // queries in its registers, in a fixed order.  w_j is fp32, so the queries
-// enter as hi + lo (two products into one accumulator): 4 D flop per pair, on
-// the tensor cores while the CUDA cores take 2^(s - lse), one MUFU operation a
-// pair, 1024 clocks a tile for either.
+// enter as hi + lo (two products into one accumulator): 4 D flop per pair on
+// the tensor cores, 1024 clocks a tile, while the CUDA cores take 2^(s - lse), one
+// MUFU operation a pair, 1024 clocks a tile too.  Shared memory must not be a
+// third bound of more: with both operands there a product of 128 x 128 reads
+// its full bandwidth (1536 clocks a tile with the copies' writes).  So the keys,
+// which stay for the whole kernel, go into TMEM as operand A, and a CTA takes
+// two key tiles, which meet every query tile one after the other: 768 clocks.
 #include <algorithm>
 #include <type_traits>
 
@@ -713,17 +717,19 @@ __global__ void __launch_bounds__(256) kv4_chunk_combine_kernel(const FwdParams4
 template <int D>
 struct WLayout {
   static constexpr int kTile = 128 * D * 2;
-  static constexpr int kK = 0;
-  static constexpr int kQ = kTile;                         // stages of (hi, lo)
+  static constexpr int kK = 0;                             // two key tiles
+  static constexpr int kQ = 2 * kTile;                     // stages of (hi, lo)
   static constexpr int kLse = kQ + kStages * 2 * kTile;    // 4 x 128 floats
   static constexpr int kSum = kLse + 4 * 512;              // 128 floats
   static constexpr int kBars = kSum + 512;
-  static constexpr int kTmemSlot = kBars + 20 * 8;
+  static constexpr int kTmemSlot = kBars + 22 * 8;
   static constexpr int kAlloc = kTmemSlot + 16 + 1024;
 };
 
+constexpr int kSBufs = 3;   // TMEM: the two key tiles in 2 x 64 columns, then 3 accumulators of 128
+
 struct WBars {
-  uint64_t k_full, q_full[kStages], q_empty[kStages], s_full[4], s_empty[4], lse_full[4];
+  uint64_t k_full, a_ready, q_full[kStages], q_empty[kStages], s_full[kSBufs], s_empty[kSBufs], lse_full[4], lse_empty[4];
 };
 
 template <int D>
@@ -736,27 +742,32 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
   WBars* bars = reinterpret_cast<WBars*>(smem + L::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.x, bh = blockIdx.y, split = blockIdx.z;
+  const int tile = blockIdx.x * 2, bh = blockIdx.y, split = blockIdx.z;
   const int b = bh / p.c.heads;
   const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
   if (tile * 128 >= len) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
+  const int n_kt = (tile + 1) * 128 < len ? 2 : 1;   // key tiles
   const int q_tiles = p.rows_pad / 128;
   const int q_begin = (int)((int64_t)q_tiles * split / p.n_splits);
   const int n = (int)((int64_t)q_tiles * (split + 1) / p.n_splits) - q_begin;   // >= 1: n_splits <= q_tiles
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->k_full, 1);
+    mbar_init(&bars->a_ready, 128 * n_kt);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_empty[i], 128);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->lse_full[i], 1);
+      mbar_init(&bars->lse_empty[i], 128 * n_kt);
     }
     fence_mbar_init();
   }
@@ -777,11 +788,12 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
 
   if (warp == 9) {
     if (elect_one()) {
-      mbar_arrive_expect_tx(&bars->k_full, L::kTile);
-      for (int box = 0; box < D / 64; ++box)
-        tma_load_4d(smem + L::kK + box * 16384, &tm_k, &bars->k_full, box * 64, 0, tile * 128, bh);
+      mbar_arrive_expect_tx(&bars->k_full, n_kt * L::kTile);
+      for (int t = 0; t < n_kt; ++t)
+        for (int box = 0; box < D / 64; ++box)
+          tma_load_4d(smem + L::kK + t * L::kTile + box * 16384, &tm_k, &bars->k_full, box * 64, 0, (tile + t) * 128, bh);
       for (int j = 0; j < n; ++j) {
-        const int st = j % kStages, row = (q_begin + j) * 128;
+        const int st = j % kStages, row = (q_begin + j) * 128, sl = j & 3;
         if (!mbar_wait(&bars->q_empty[st], ((j / kStages) & 1) ^ 1, p.status, kErrWQEmpty)) break;
         mbar_arrive_expect_tx(&bars->q_full[st], 2 * L::kTile);
         uint8_t* dst = smem + L::kQ + st * 2 * L::kTile;
@@ -789,8 +801,7 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
           tma_load_4d(dst + box * 16384, &tm_qh, &bars->q_full[st], box * 64, 0, row, bh);
           tma_load_4d(dst + L::kTile + box * 16384, &tm_ql, &bars->q_full[st], box * 64, 0, row, bh);
         }
-        const int sl = j & 3;
-        if (!mbar_wait(&bars->s_empty[sl], ((j >> 2) & 1) ^ 1, p.status, kErrWSEmpty)) break;
+        if (!mbar_wait(&bars->lse_empty[sl], ((j >> 2) & 1) ^ 1, p.status, kErrWLse)) break;
         mbar_arrive_expect_tx(&bars->lse_full[sl], 512);
         bulk_load(smem + L::kLse + sl * 512, p.neg_lse + (int64_t)bh * p.rows_pad + row, 512, &bars->lse_full[sl]);
       }
@@ -798,70 +809,102 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
   } else if (warp == 8) {
     if (elect_one()) {
       constexpr uint32_t idesc = make_idesc_f16(128, 128, false);
-      const uint32_t k_base = smem_u32(smem + L::kK), q_base = smem_u32(smem + L::kQ);
-      bool ok = mbar_wait(&bars->k_full, 0, p.status, kErrWK);
+      const uint32_t q_base = smem_u32(smem + L::kQ);
+      bool ok = mbar_wait(&bars->a_ready, 0, p.status, kErrWK);
+      int buf = 0;
+      uint32_t phase = 0;    // of the accumulators: product number / kSBufs
       for (int j = 0; j < n && ok; ++j) {
-        const int st = j % kStages, sl = j & 3;
-        ok = mbar_wait(&bars->q_full[st], (j / kStages) & 1, p.status, kErrWQFull) &&
-             mbar_wait(&bars->s_empty[sl], ((j >> 2) & 1) ^ 1, p.status, kErrWSEmpty);
-        if (!ok) break;
-        tc_fence_after();
+        const int st = j % kStages;
+        ok = mbar_wait(&bars->q_full[st], (j / kStages) & 1, p.status, kErrWQFull);
+        for (int t = 0; t < n_kt && ok; ++t) {
+          ok = mbar_wait(&bars->s_empty[buf], (phase & 1) ^ 1, p.status, kErrWSEmpty);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_bf16_ss(tmem + 128 * sl, make_sw128_desc(k_base + off, 16, 1024),
-                        make_sw128_desc(q_base + (st * 2 + part) * L::kTile + off, 16, 1024), idesc,
-                        part > 0 || kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              mma_bf16_ts(tmem + 128 + 128 * buf, tmem + 64 * t + kk * 8,
+                          make_sw128_desc(q_base + (st * 2 + part) * L::kTile + off, 16, 1024), idesc, part > 0 || kk > 0);
+            }
+          if (t == n_kt - 1) mma_commit(&bars->q_empty[st]);
+          mma_commit(&bars->s_full[buf]);
+          if (++buf == kSBufs) {
+            buf = 0;
+            ++phase;
           }
-        mma_commit(&bars->q_empty[st]);
-        mma_commit(&bars->s_full[sl]);
+        }
       }
     }
   } else {
-    // warpgroup w takes the query tiles j = w, w + 2, ...; thread i owns key i of the tile
+    // warpgroup w takes the products w, w + 2, ... (with two key tiles: all those
+    // of tile w; with one: every second query tile); thread i owns key i of the tile
     const int w = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     uint64_t s2[4] = {0, 0, 0, 0};
     bool ok = true;
-    for (int j = w; j < n; j += 2) {
-      const int sl = j & 3;
+    if (w < n_kt) {   // the key's row into TMEM, pairs of features to a column
+      ok = warp_wait(&bars->k_full, 0, ok, p.status, kErrWK);
+      if (ok) {
+        const uint8_t* src = smem + L::kK + w * L::kTile;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t a[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + h * 16384 + sw128_offset(r, c * 8));
+            a[4 * c] = v.x; a[4 * c + 1] = v.y; a[4 * c + 2] = v.z; a[4 * c + 3] = v.w;
+          }
+          tmem_st32(tmem + lane_base + 64 * w + h * 32, a);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->a_ready);
+      }
+    }
+    const int total = n * n_kt;
+    for (int i = w; i < total; i += 2) {
+      const int j = n_kt == 2 ? i >> 1 : i, sl = j & 3, buf = i % kSBufs;
       ok = warp_wait(&bars->lse_full[sl], (j >> 2) & 1, ok, p.status, kErrWLse);
-      ok = warp_wait(&bars->s_full[sl], (j >> 2) & 1, ok, p.status, kErrWSFull);
+      ok = warp_wait(&bars->s_full[buf], (i / kSBufs) & 1, ok, p.status, kErrWSFull);
       if (!ok) break;
       tc_fence_after();
       const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + L::kLse + sl * 512);
       uint32_t raw[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + 128 * sl + c * 32, raw[c]);
+      for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + 128 + 128 * buf + c * 32, raw[c]);
       tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&bars->s_empty[buf]);   // the scores are in registers
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const ulonglong2 n2 = nl[c * 8 + i];   // -lse of four queries (the same for every key)
-          const uint64_t a = f2_add(f2_pack(__uint_as_float(raw[c][4 * i]), __uint_as_float(raw[c][4 * i + 1])), n2.x);
-          const uint64_t e = f2_add(f2_pack(__uint_as_float(raw[c][4 * i + 2]), __uint_as_float(raw[c][4 * i + 3])), n2.y);
+        for (int k = 0; k < 8; ++k) {
+          const ulonglong2 n2 = nl[c * 8 + k];   // -lse of four queries (the same for every key)
+          const uint64_t a = f2_add(f2_pack(__uint_as_float(raw[c][4 * k]), __uint_as_float(raw[c][4 * k + 1])), n2.x);
+          const uint64_t e = f2_add(f2_pack(__uint_as_float(raw[c][4 * k + 2]), __uint_as_float(raw[c][4 * k + 3])), n2.y);
           float a0, a1, e0, e1;
           f2_unpack(a, a0, a1);
           f2_unpack(e, e0, e1);
-          s2[2 * (i & 1)] = f2_add(s2[2 * (i & 1)], f2_pack(fast_exp2(a0), fast_exp2(a1)));
-          s2[2 * (i & 1) + 1] = f2_add(s2[2 * (i & 1) + 1], f2_pack(fast_exp2(e0), fast_exp2(e1)));
+          s2[2 * (k & 1)] = f2_add(s2[2 * (k & 1)], f2_pack(fast_exp2(a0), fast_exp2(a1)));
+          s2[2 * (k & 1) + 1] = f2_add(s2[2 * (k & 1) + 1], f2_pack(fast_exp2(e0), fast_exp2(e1)));
         }
-      tc_fence_before();
-      mbar_arrive(&bars->s_empty[sl]);
+      mbar_arrive(&bars->lse_empty[sl]);
     }
     float t[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) f2_unpack(s2[i], t[2 * i], t[2 * i + 1]);
-    const float total = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+    float x = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
     float* sum = reinterpret_cast<float*>(smem + L::kSum);
-    if (w == 1) sum[r] = total;
-    named_bar_sync(1, 256);
-    if (w == 0 && ok && tile * 128 + r < len) {
-      const float x = total + sum[r];
-      const int64_t at = (int64_t)bh * p.c.cap + tile * 128 + r;
+    if (n_kt == 1) {   // both warpgroups hold parts of the one tile
+      if (w == 1) sum[r] = x;
+      named_bar_sync(1, 256);
+      if (w == 0) x += sum[r];
+    }
+    const int key = (tile + (n_kt == 2 ? w : 0)) * 128 + r;
+    if ((n_kt == 2 || w == 0) && ok && key < len) {
+      const int64_t at = (int64_t)bh * p.c.cap + key;
       if (p.n_splits > 1) {
         p.part_o[(int64_t)split * p.c.batch * p.c.heads * p.c.cap + at] = x;
       } else {
@@ -944,7 +987,7 @@ cudaError_t chunk_weights_d(const CUtensorMap& tqh, const CUtensorMap& tql, cons
   cudaError_t e = allow_smem(kv4_chunk_weights_kernel<D>, WLayout<D>::kAlloc, have);
   if (e != cudaSuccess) return e;
   const int BH = p.c.batch * p.c.heads;
-  e = launch_early(kv4_chunk_weights_kernel<D>, dim3(p.c.cap / 128, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s, tqh,
+  e = launch_early(kv4_chunk_weights_kernel<D>, dim3((p.c.cap + 255) / 256, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s, tqh,
                    tql, tk, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
   kv4_weights_sum_kernel<<<dim3((p.c.cap + 255) / 256, BH), 256, 0, s>>>(p);
@@ -965,9 +1008,9 @@ bool chunk_units_fit(const Cache& c, int rows) {
   return units < (int64_t(1) << 30) && (int64_t)c.cap / 128 * 148 < (int64_t(1) << 31);
 }
 
-// Parts of the queries, for the weights: a CTA takes a key tile.
+// Parts of the queries, for the weights: a CTA takes two key tiles.
 int chunk_weight_splits(const Cache& c, int rows_pad) {
-  const int64_t units = (int64_t)c.batch * c.heads * (c.cap / 128);
+  const int64_t units = (int64_t)c.batch * c.heads * ((c.cap + 255) / 256);
   const int64_t want = std::max<int64_t>(1, 148 / units);
   return (int)std::min<int64_t>({want, (int64_t)rows_pad / 128, (int64_t)32});
 }
