@@ -30,7 +30,7 @@ namespace kv4 {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 
 // Order-preserving integer of a weight.
@@ -40,21 +40,26 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 40 * 1024;   // keys a CTA keeps; longer runs are read again each time
 
 struct SelShared {
   uint32_t hist[kBins];      // this CTA's counts
   uint32_t total[3][kBins];  // the cluster's
-  uint32_t scan[kSelThreads / 32];
-  uint32_t warp_gt[kSelThreads / 32], warp_eq[kSelThreads / 32];
+  uint32_t scan[kSelWarps];
+  uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
   uint32_t cta_gt, cta_eq;
   uint32_t bin, above;
 };
 
+// Candidates of a CTA, and of one of its warps (a multiple of 128: a lane takes
+// four neighbours at a time).
+__host__ __device__ constexpr int cta_run(int n) { return (n + kCluster * 32 - 1) / (kCluster * 32) * 32; }
+__host__ __device__ constexpr int warp_run(int cta) { return (cta + kSelThreads * 4 - 1) / (kSelThreads * 4) * 128; }
+
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) kv4_select_kernel(const EvictParams p, bool held) {
   extern __shared__ __align__(16) uint8_t sel_smem[];
   SelShared& sh = *reinterpret_cast<SelShared*>(sel_smem);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelShared));
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -66,18 +71,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   const int need = kept - rec;
   const float* w = p.w_src + (int64_t)bh * p.src.cap;
   int32_t* index = p.index + (int64_t)bh * p.keep;
-  const int seg = (n + kCluster * 32 - 1) / (kCluster * 32) * 32;
-  const int i0 = min(rank * seg, n), i1 = min(i0 + seg, n);
+  const int seg = cta_run(n), run = warp_run(seg);
+  // this warp's candidates: [a0, a0 + len_w), in steps of 128, a lane four of them
+  const int i1 = min((rank + 1) * seg, n), a0 = rank * seg + warp * run;
+  const int len_w = min(run, i1 - a0);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelShared)) + warp * run;
+
+  // the keys of four neighbours; 0, which no weight has, behind the last (the
+  // row has 128-slot granularity, so reading four is always inside it)
+  auto from_row = [&](int o) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(w + a0 + o));
+    return make_uint4(order_key(x.x), o + 1 < len_w ? order_key(x.y) : 0u, o + 2 < len_w ? order_key(x.z) : 0u,
+                      o + 3 < len_w ? order_key(x.w) : 0u);
+  };
+  if (held) {
+#pragma unroll 4
+    for (int o = lane * 4; o < len_w; o += 128) *reinterpret_cast<uint4*>(keys + o) = from_row(o);
+  }
+  auto four = [&](int o) {
+    if (o >= len_w) return make_uint4(0, 0, 0, 0);
+    return held ? *reinterpret_cast<const uint4*>(keys + o) : from_row(o);
+  };
 
   // the need-th largest key and how many of those equal to it stay
-  uint32_t top = need == 0 ? 0xffffffffu : 0u;   // all stay: every key is above or equal
-  uint32_t ties = need == 0 ? 0u : 0x7fffffffu;
-  if (held)
-    for (int i = i0 + tid * 4; i < i1; i += kSelThreads * 4) {   // i0 and the row are multiples of 4 (or past n)
-      const float4 x = __ldg(reinterpret_cast<const float4*>(w + i));
-      *reinterpret_cast<uint4*>(keys + (i - i0)) = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
-    }
-  auto key_at = [&](int i) { return held ? keys[i - i0] : order_key(__ldg(w + i)); };
+  uint32_t top = need == 0 ? 0xffffffffu : 0u;   // all stay: every key is above
+  uint32_t ties = 0;
   if (need > 0 && need < n) {                    // the same for the whole cluster
     uint32_t prefix = 0, left = (uint32_t)need;
     for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = sh.total[0][i] = sh.total[1][i] = sh.total[2][i] = 0;
@@ -86,19 +104,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int bits = pass == 2 ? 10 : 11;
-      for (int i = i0 + tid; i < i1; i += kSelThreads) {
-        const uint32_t key = key_at(i);
-        if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&sh.hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+      auto count = [&](uint32_t key) {
+        if (key != 0 && (pass == 0 || (key >> (shift + bits)) == prefix))
+          atomicAdd(&sh.hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+      };
+      for (int o = lane * 4; o < len_w; o += 128) {
+        const uint4 k = four(o);
+        count(k.x);
+        count(k.y);
+        count(k.z);
+        count(k.w);
       }
       __syncthreads();
       for (int i = tid; i < kBins; i += kSelThreads) {
         const uint32_t v = sh.hist[i];
         if (v == 0) continue;
         sh.hist[i] = 0;
+#pragma unroll
         for (int r = 0; r < kCluster; ++r) atomicAdd(cluster.map_shared_rank(&sh.total[pass][i], r), v);
       }
       cluster.sync();
-      // thread t holds the counts of bins 4t .. 4t+3 from the top
+      // thread t holds the counts of its bins from the top
       constexpr int kPer = kBins / kSelThreads;
       uint32_t cnt[kPer], mine = 0;
 #pragma unroll
@@ -111,8 +137,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
       }
       if (lane == 31) sh.scan[warp] = incl;
       __syncthreads();
-      uint32_t before = incl - mine;
-      for (int k = 0; k < warp; ++k) before += sh.scan[k];
+      uint32_t before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[lane] : 0u);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (before < left && before + cnt[k] >= left) {   // exactly one bin
@@ -127,56 +152,60 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
     }
     top = prefix;
     ties = left;
-  } else {
-    __syncthreads();
   }
+  __syncwarp();
 
-  // number the kept tokens of this CTA's run, warp by warp
-  const int wseg = ((i1 - i0) + kSelThreads - 1) / kSelThreads * 32;
-  const int a0 = min(i0 + warp * wseg, i1), a1 = min(a0 + wseg, i1);
+  // number the kept tokens, warp by warp
   uint32_t gt = 0, eq = 0;
-  for (int i = a0; i < a1; i += 32) {
-    const uint32_t key = i + lane < a1 ? key_at(i + lane) : 0u;
-    const bool in = i + lane < a1;
-    gt += __popc(__ballot_sync(0xffffffffu, in && key > top));
-    eq += __popc(__ballot_sync(0xffffffffu, in && key == top));
+  for (int o = lane * 4; o < len_w; o += 128) {
+    const uint4 k = four(o);
+    gt += (k.x > top) + (k.y > top) + (k.z > top) + (k.w > top);
+    eq += (k.x == top) + (k.y == top) + (k.z == top) + (k.w == top);   // (behind the last: 0, and top > 0 or no ties)
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     sh.warp_gt[warp] = gt;
     sh.warp_eq[warp] = eq;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t a = 0, e = 0;
-    for (int k = 0; k < kSelThreads / 32; ++k) {
-      a += sh.warp_gt[k];
-      e += sh.warp_eq[k];
+  if (warp == 0) {
+    const uint32_t g = __reduce_add_sync(0xffffffffu, sh.warp_gt[lane]), e = __reduce_add_sync(0xffffffffu, sh.warp_eq[lane]);
+    if (lane == 0) {
+      sh.cta_gt = g;
+      sh.cta_eq = e;
     }
-    sh.cta_gt = a;
-    sh.cta_eq = e;
   }
   cluster.sync();
-  uint32_t gt0 = 0, eq0 = 0;
-  for (int r = 0; r < rank; ++r) {
-    gt0 += *cluster.map_shared_rank(&sh.cta_gt, r);
-    eq0 += *cluster.map_shared_rank(&sh.cta_eq, r);
-  }
+  uint32_t gt0 = lane < rank ? *cluster.map_shared_rank(&sh.cta_gt, lane) : 0u;
+  uint32_t eq0 = lane < rank ? *cluster.map_shared_rank(&sh.cta_eq, lane) : 0u;
+  gt0 = __reduce_add_sync(0xffffffffu, gt0 + (lane < warp ? sh.warp_gt[lane] : 0u));
+  eq0 = __reduce_add_sync(0xffffffffu, eq0 + (lane < warp ? sh.warp_eq[lane] : 0u));
   cluster.sync();   // no CTA leaves while its shared memory is read
-  for (int k = 0; k < warp; ++k) {
-    gt0 += sh.warp_gt[k];
-    eq0 += sh.warp_eq[k];
-  }
   const uint32_t below = (1u << lane) - 1u;
-  for (int i = a0; i < a1; i += 32) {
-    const bool in = i + lane < a1;
-    const uint32_t key = in ? key_at(i + lane) : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, in && key > top);
-    const uint32_t me = __ballot_sync(0xffffffffu, in && key == top);
-    const uint32_t eq_rank = eq0 + __popc(me & below);
-    if (in && (key > top || (key == top && eq_rank < ties)))
-      index[gt0 + __popc(mg & below) + min(eq_rank, ties)] = i + lane;
-    gt0 += __popc(mg);
-    eq0 += __popc(me);
+  for (int o0 = 0; o0 < len_w; o0 += 128) {
+    const int o = o0 + lane * 4;
+    const uint4 k4 = four(o);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    uint32_t g = gt0, e = eq0;   // before this lane's first
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t mg = __ballot_sync(0xffffffffu, k[c] > top), me = __ballot_sync(0xffffffffu, k[c] == top);
+      g += __popc(mg & below);
+      e += __popc(me & below);
+      gt0 += __popc(mg);
+      eq0 += __popc(me);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (k[c] > top) {
+        index[g + min(e, ties)] = a0 + o + c;
+        ++g;
+      } else if (k[c] == top) {
+        if (e < ties) index[g + e] = a0 + o + c;
+        ++e;
+      }
+    }
   }
   for (int i = rank * kSelThreads + tid; i < p.keep - need; i += kCluster * kSelThreads)
     index[need + i] = i < rec ? n + i : -1;
@@ -271,12 +300,13 @@ __global__ void __launch_bounds__(256) kv4_move_kernel(const EvictParams p) {
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   const int BH = p.src.batch * p.src.heads;
   // room for the keys of an eighth of a full cache, if that is not too much
-  const int seg = (p.src.cap + kCluster * 32 - 1) / (kCluster * 32) * 32;
-  const int bytes = (int)sizeof(SelShared) + (seg <= kSelKeys ? seg * 4 : 0);
+  const int keys = kSelWarps * warp_run(cta_run(p.src.cap));
+  const bool held = keys <= kSelKeys;
+  const int bytes = (int)sizeof(SelShared) + (held ? keys * 4 : 0);
   static SmemRecord have;
   cudaError_t e = allow_smem(kv4_select_kernel, bytes, have);
   if (e != cudaSuccess) return e;
-  kv4_select_kernel<<<dim3(kCluster, BH), kSelThreads, bytes, s>>>(p, seg <= kSelKeys);
+  kv4_select_kernel<<<dim3(kCluster, BH), kSelThreads, bytes, s>>>(p, held);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
