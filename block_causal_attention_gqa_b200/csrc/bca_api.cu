@@ -15,6 +15,7 @@
 
 #include "../../include/magi_bca.h"
 #include "bca_kernels.h"
+#include "bca_kv4.h"
 #include "bca_sched.h"
 #include "sm100.cuh"
 
@@ -456,7 +457,7 @@ const char* magi_bca_status_string(int status) {
     case MAGI_BCA_WORKSPACE_TOO_SMALL: return "workspace too small";
     case MAGI_BCA_CUDA_ERROR: return "CUDA runtime error";
     case MAGI_BCA_DEVICE_TIMEOUT: return "device-side wait timed out";
-    case MAGI_BCA_DEVICE_CHECK: return "device-side bounds check failed (debug build)";
+    case MAGI_BCA_DEVICE_CHECK: return "device-side bounds check failed";
     default: return "unknown status";
   }
 }
@@ -728,7 +729,10 @@ int magi_bca_last_device_status(void) {
   if (cudaMemcpyFromSymbol(&host, g_device_status, sizeof(int)) != cudaSuccess) return MAGI_BCA_CUDA_ERROR;
   const int zero = 0;
   if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess) return MAGI_BCA_CUDA_ERROR;
-  if (host == 0) return MAGI_BCA_OK;
+  int position = 0;   // an append to the 4-bit cache outside of it
+  const int st = kv4::take_position_status(&position);
+  if (st != MAGI_BCA_OK) return st;
+  if (host == 0) return position == 0 ? MAGI_BCA_OK : MAGI_BCA_DEVICE_CHECK;
   return host >= 3000 && host < 3100 ? MAGI_BCA_DEVICE_CHECK : MAGI_BCA_DEVICE_TIMEOUT;
 }
 

@@ -13,8 +13,9 @@
 namespace magi {
 namespace kv4 {
 
-// Device status codes of positions outside the cache (read as MAGI_BCA_DEVICE_CHECK).
+// Code of a position outside the cache (read as MAGI_BCA_DEVICE_CHECK), and its word, read and cleared.
 enum : int { kErrPosition = 3050 };
+int take_position_status(int* code);
 
 // The cache with its strides; see magi_bca_kv4_cache.
 struct Cache {

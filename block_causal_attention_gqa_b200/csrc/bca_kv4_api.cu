@@ -11,6 +11,18 @@
 
 namespace magi {
 namespace kv4 {
+
+// Set by appends to a slot outside the cache.  A word of its own: the waits of
+// running kernels give up once the status word is set.
+__device__ int g_position_status;
+
+int take_position_status(int* code) {
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(code, g_position_status, sizeof(int)) != cudaSuccess) return MAGI_BCA_CUDA_ERROR;
+  if (*code != 0 && cudaMemcpyToSymbol(g_position_status, &zero, sizeof(int)) != cudaSuccess) return MAGI_BCA_CUDA_ERROR;
+  return MAGI_BCA_OK;
+}
+
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -32,10 +44,24 @@ Cache to_cache(const magi_bca_kv4_cache& c) {
   return Cache{c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.batch, c.heads_kv, c.head_dim, c.capacity};
 }
 
-// Which kernels: the token kernels convert the cache once for each 8 rows (fwd)
-// or once in all (weights), the chunk kernels expand it to fp16 first.
-constexpr int kTokenFwdRows = 32;
-constexpr int kTokenWeightRows = 64;
+// Which kernels.  The token kernels convert the cache once for each 8 rows (fwd)
+// or once in all (weights) and read nothing else; the chunk kernels expand it
+// to fp16 first and then take any number of rows at the tensor cores' rate.
+// Times in us (token / chunk; head_dim 128, one batch element):
+//   fwd, 8 heads x 92160 tokens:   48 rows 127 / 182,  63 rows 164 / 181,  96 rows 240 / 182
+//        8 heads x 16384 tokens:   63 rows  40 /  58,  96 rows  55 /  59, 126 rows  69 /  59
+//        2 heads x 92160 tokens:   64 rows  49 / 104,  96 rows  69 / 104, 128 rows  87 /  98
+//        8 heads x  2048 tokens:  126 rows  16 /  23, 192 rows  20 /  28
+//   weights, 8 heads x 92160:      63 rows 117 / 177,  96 rows 169 / 177, 126 rows 219 / 177
+//        2 heads x 92160:          48 rows  28 /  45,  64 rows  50 /  44
+//        8 heads x 16384:          30 rows  24 /  34,  48 rows  34 /  34,  63 rows  46 /  34
+//        8 heads x 2048:           30 rows 10.3 / 10.9, 48 rows 13.3 / 10.6
+bool use_token_kernels(const magi_bca_kv4_cache& c, int rows, bool weights) {
+  const int64_t slots = (int64_t)c.batch * c.heads_kv * c.capacity;
+  if (weights) return rows <= (slots >= 262144 ? 80 : 40);
+  return rows <= (slots <= 32768 ? 192 : slots <= 262144 ? 96 : 64);
+}
+constexpr int kMostTokenRows = 192;
 
 int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
   if (q == nullptr || q->seqlen_q < 1 || q->heads_q < 1) return MAGI_BCA_INVALID_ARG;
@@ -45,7 +71,7 @@ int check_query(const magi_bca_kv4_cache& c, const magi_bca_kv4_query* q) {
   if (q->heads_q % c.heads_kv != 0) return MAGI_BCA_UNSUPPORTED;
   if ((int64_t)c.batch * q->heads_q * q->seqlen_q >= (int64_t(1) << 31)) return MAGI_BCA_UNSUPPORTED;
   const int rows = q->heads_q / c.heads_kv * q->seqlen_q;
-  if (!token_steps_fit(to_cache(c), std::min(rows, kTokenWeightRows)) || !chunk_units_fit(to_cache(c), rows))
+  if (!token_steps_fit(to_cache(c), std::min(rows, kMostTokenRows)) || !chunk_units_fit(to_cache(c), rows))
     return MAGI_BCA_UNSUPPORTED;
   return MAGI_BCA_OK;
 }
@@ -69,7 +95,7 @@ Plan plan_of(const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, bool weig
     p.total += (bytes + 255) / 256 * 256;
     return at;
   };
-  p.token = rows <= (weights ? kTokenWeightRows : kTokenFwdRows);
+  p.token = use_token_kernels(c, rows, weights);
   p.rows_pad = (int)(((int64_t)rows + 127) / 128 * 128);
   auto pieces = [&](int64_t n) {
     p.part_o = take((size_t)n * D * 4);
@@ -143,8 +169,13 @@ int magi_bca_kv4_append(const magi_bca_bf16* k, const magi_bca_bf16* v, const ma
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(rope_k, 16) || rope_batch_stride % 4 != 0) return MAGI_BCA_INVALID_ARG;
   if (n_tokens > (1 << 30)) return MAGI_BCA_UNSUPPORTED;
   AppendParams p = {};
-  st = device_status_word(&p.status);
+  int* status;
+  st = device_status_word(&status);   // checks the device
   if (st != MAGI_BCA_OK) return st;
+  void* word = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&word, g_position_status);
+  if (e != cudaSuccess) return done("status word", e);
+  p.status = static_cast<int*>(word);
   p.c = to_cache(*cache);
   p.k = k;
   p.v = v;

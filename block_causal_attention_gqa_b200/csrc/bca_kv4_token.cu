@@ -730,22 +730,29 @@ int64_t histories(const Cache& c, int rows, bool weights) {
 }  // namespace
 
 // CTAs of the token kernels: as many as run at once (4 an SM, 3 with two row
-// groups), but no more than have a step for each warp if the cache is full.
+// groups or where the weights' queries fill shared memory), but no more than
+// have a step for each warp if the cache is full.
 int token_ctas(const Cache& c, int rows, bool weights) {
   const int64_t useful = histories(c, rows, weights) * ((c.cap + kStep * kWarps - 1) / (kStep * kWarps));
-  return (int)std::min<int64_t>(useful, 148 * (weights || row_tile(rows) == 4 ? 4 : 3));
+  int per_sm = row_tile(rows) == 4 ? 4 : 3;
+  if (weights) {
+    const int bytes = c.dim == 128 ? RingW<128>::bytes((rows + 3) / 4) : RingW<64>::bytes((rows + 3) / 4);
+    per_sm = std::max(1, std::min(4, 227 * 1024 / (bytes + 1024)));
+  }
+  return (int)std::min<int64_t>(useful, 148 * per_sm);
 }
 
 // CTAs of the cluster that takes a history, 0 where histories are laid end to
-// end instead.  As many (a power of two) as let all clusters run at once, and
-// no more than have a step for each warp; histories of more than 8 steps a warp
-// are left to the balanced split, which then costs less than the uneven ends of
-// clusters.
+// end instead.  As many (a power of two) as let all clusters run at once (16 only
+// with a CTA an SM: with more, clusters of 16 wait for one another; 24 of them
+// took 15.5 us where 32 of 8 took 9.2), and no more than have a step for each
+// warp.  Histories of more than 8 steps a warp are left to the balanced split,
+// which then costs less than the uneven ends of clusters.
 int token_cluster(const Cache& c, int rows) {
   const int64_t slots = 148 * (row_tile(rows) == 4 ? 4 : 3), hist = histories(c, rows, false);
   const int steps = (c.cap + kStep - 1) / kStep;
   int size = 1;
-  while (size < 16 && hist * size * 2 <= slots && steps > kWarps * size) size *= 2;
+  while (size < 16 && hist * size * 2 <= (size == 8 ? 148 : slots) && steps > kWarps * size) size *= 2;
   return steps <= 8 * kWarps * size ? size : 0;
 }
 

@@ -323,8 +323,12 @@ int64_t magi_bca_bwd_schedule(const int32_t* q_chunk_offsets, const int32_t* kv_
  * device memory, so that a captured graph replays with growing histories.
  * Slots from `length` on may hold anything and are neither read for a result
  * nor written by any call but append.  No call allocates, synchronises or
- * copies; all can be captured in a CUDA graph.  Calls that use the same cache
- * or workspace must be ordered (one stream, or events). */
+ * copies, so all can be captured in a CUDA graph (after a first call of their
+ * kind on the device, which loads the kernels).  Calls that use the same cache
+ * or workspace must be ordered (one stream, or events).
+ *
+ * Tensors otherwise as above: contiguous, q, k, v, out and base_out bf16 and
+ * 16-byte aligned, gammas fp32 [head_dim]. */
 typedef struct {
   uint8_t* k_codes;  /* [batch, heads_kv, capacity, head_dim / 2]: byte i holds feature 2i in its low half
                       * and 2i + 1 in its high half */
@@ -352,10 +356,10 @@ typedef struct {
  * are device int32 [batch]; counts (NULL: n_tokens everywhere) is how many of
  * the tokens are real, the rest is padding and not written.  rope_k [n_tokens,
  * head_dim/2] (or one such table for each batch element, rope_batch_stride
- * apart, a multiple of 4) are the tokens' angles, 16-byte aligned, or NULL.  Angles are taken in fp32 up to
- * 10^9 in magnitude.  Overwriting slots is allowed.  A
- * token whose slot is outside the cache is not written and sets
- * MAGI_BCA_DEVICE_CHECK in the device status word. */
+ * apart, a multiple of 4) are the tokens' angles in radians (up to 10^9, 16-byte
+ * aligned), or NULL.  Overwriting slots is allowed.  A token whose slot is
+ * outside the cache is not written; magi_bca_last_device_status then reports
+ * MAGI_BCA_DEVICE_CHECK. */
 int magi_bca_kv4_append(const magi_bca_bf16* k, const magi_bca_bf16* v, const magi_bca_kv4_cache* cache,
                         const int32_t* start, const int32_t* counts, int32_t n_tokens, const float* rope_k,
                         int64_t rope_batch_stride, float rms_eps, void* stream);

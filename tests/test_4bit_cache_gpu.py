@@ -171,9 +171,11 @@ FEW = [(1, 1, 1, 1, 64, 128, [1]), (1, 1, 2, 1, 128, 128, [33]), (2, 1, 4, 2, 12
        (1, 8, 4, 1, 128, 640, [600]), (1, 1, 24, 8, 128, 9216, [9001]), (4, 2, 10, 5, 64, 128, [5, 64, 65, 128]),
        # histories long enough to be laid end to end over the CTAs (the others take a cluster each)
        (1, 1, 2, 1, 128, 20480, [20001]), (3, 2, 4, 1, 64, 17536, [17, 0, 17500]), (2, 1, 3, 1, 64, 65536, [65536, 40000]),
-       (5, 1, 2, 2, 128, 16512, [1, 16512, 0, 9000, 333]), (1, 5, 6, 1, 128, 16640, [16639])]
-MANY = [(1, 33, 1, 1, 64, 128, [1]), (1, 40, 2, 1, 128, 384, [257]), (2, 129, 4, 2, 128, 512, [512, 0]),
-        (1, 100, 24, 8, 128, 1152, [1050]), (3, 65, 3, 3, 64, 256, [255, 128, 7]), (1, 513, 4, 2, 64, 2560, [2433]),
+       (5, 1, 2, 2, 128, 16512, [1, 16512, 0, 9000, 333]), (1, 5, 6, 1, 128, 16640, [16639]),
+       (1, 64, 1, 1, 128, 33024, [32900]), (1, 33, 1, 1, 64, 128, [1]), (1, 40, 2, 1, 128, 384, [257]),
+       (1, 90, 4, 2, 64, 256, [255])]
+MANY = [(1, 193, 1, 1, 64, 128, [1]), (1, 97, 2, 1, 128, 384, [257]), (2, 129, 4, 2, 128, 512, [512, 0]),
+        (1, 100, 24, 8, 128, 1152, [1050]), (3, 200, 3, 3, 64, 256, [255, 128, 7]), (1, 513, 4, 2, 64, 2560, [2433]),
         (1, 300, 16, 4, 128, 4096, [4096])]
 
 
@@ -231,7 +233,7 @@ def test_attention_with_scores_that_grow_along_the_history(Sq):
 
 def test_a_query_that_is_nan_gives_nan_and_no_other_row_does():
     g = gen(9)
-    for Sq in (3, 80):
+    for Sq in (3, 200):
         cache = filled(g, 1, 2, 128, 256, [200])
         q = randn(g, 1, Sq, 4, 128).bfloat16()
         q[0, 1, 2, 5] = math.nan
@@ -254,7 +256,7 @@ def test_lengths_beyond_the_cache_are_clamped():
 
 # ------------------------------------------------------------------- weights
 @pytest.mark.parametrize("decay", [1.0, 0.0, 0.5])
-@pytest.mark.parametrize("case", [FEW[0], FEW[2], FEW[4], FEW[5], FEW[7], FEW[8]] + MANY)
+@pytest.mark.parametrize("case", FEW + MANY)
 def test_weights(case, decay):
     B, Sq, Hq, H, D, cap, lengths = case
     g = gen(sum(case[:6]) + 1)
@@ -319,6 +321,20 @@ def test_evict(B, H, D, cap, lengths, keep, recent, dst_cap, kind):
                 assert torch.equal(new[b, h, m:], first[b, h, m:])      # slots behind are left as they were
             assert torch.equal(tw[b, h, :m].nan_to_num(-1, 2e38, -2e38), w[b, h, src].nan_to_num(-1, 2e38, -2e38))
             assert (tw[b, h, m:] == 7).all()
+
+
+def test_evict_from_a_history_longer_than_shared_memory_holds():
+    g = gen(41)
+    n, keep = 330001, 5001
+    cap = -(-n // 128) * 128
+    cache = bca.magi_bca_kv4_cache(1, 1, 64, cap)
+    cache.k_codes.random_(0, 256, generator=g)
+    w = torch.round(torch.exp(2 * randn(g, 1, 1, cap)) * 64) / 64
+    to, tw = bca.magi_bca_kv4_cache(1, 1, 64, keep), torch.zeros(1, 1, -(-keep // 128) * 128, device=DEV)
+    _, index = bca.magi_bca_kv4_evict(cache, w, ints(n), keep, 100, to, tw)
+    at = ref.kept(w[0, 0].tolist(), n, keep, 100)
+    assert index[0, 0].tolist() == at
+    assert torch.equal(to.k_codes[0, 0, :keep], cache.k_codes[0, 0, torch.tensor(at, device=DEV)])
 
 
 # ----------------------------------------------------- together, as it is used
@@ -404,11 +420,45 @@ def test_a_captured_decoding_step_replays_while_the_history_grows():
     assert bca.magi_bca_last_device_status() == 0
 
 
+def test_two_captured_chunk_steps_do_not_share_a_workspace():
+    """Two graphs of the chunk kernels, replayed at the same time on two streams."""
+    g = gen(37)
+    D, cap, Sq = 128, 2048, 300
+    gq, gk = gains(g, D)
+    jobs = []
+    for i in range(2):
+        cache = filled(g, 1, 2, D, cap, [1900 + i])
+        q = randn(g, 1, Sq, 4, D).bfloat16()
+        jobs.append((cache, q, ints(1900 + i), torch.zeros(1, 2, cap, device=DEV)))
+
+    def step(cache, q, n, w):
+        out, lse = bca.magi_bca_kv4_fwd(q, cache, n, gq, gk)
+        return out, lse, bca.magi_bca_kv4_weights(q, cache, n, lse, gq, gk, w, decay=0.0)
+
+    want = [[t.clone() for t in step(*j)] for j in jobs]
+    torch.cuda.synchronize()
+    streams, graphs, got = [torch.cuda.Stream() for _ in jobs], [], []
+    for s, j in zip(streams, jobs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got.append(step(*j))
+        graphs.append(graph)
+    for _ in range(5):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        n = 1900
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(a[2][..., :n], b[2][..., :n])
+    assert bca.magi_bca_last_device_status() == 0
+
+
 def test_calls_on_another_stream():
     g = gen(29)
     D, cap = 128, 1024
     cache = filled(g, 1, 2, D, cap, [1000])
-    q = randn(g, 1, 80, 4, D).bfloat16()
+    q = randn(g, 1, 200, 4, D).bfloat16()
     gq, gk = gains(g, D)
     n = ints(1000)
     want = bca.magi_bca_kv4_fwd(q, cache, n, gq, gk)
