@@ -19,6 +19,17 @@
 namespace magi {
 namespace kv4 {
 
+// Programmatic dependent launch.  A kernel launched with launch_early() may start
+// while the kernel before it on the stream is ending, and waits for that
+// kernel's end (and with it for all before) itself, before it reads or writes
+// anything that the kernel before touches.  What the kernel before wrote may therefore change while the grid
+// is on the device, so nothing is read through the read-only path (no __ldg).
+// Not for kernels whose CTAs share the work out in equal parts: started into the
+// gaps of a running kernel they land unevenly on the SMs (the weights of 4 x
+// 92160 tokens took 61 us so, against 48).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 constexpr int kBlock = 16;             // features that share a scale
 constexpr float kTopScale = 10240.f;   // largest scale
 constexpr uint32_t kTopScaleByte = 226;

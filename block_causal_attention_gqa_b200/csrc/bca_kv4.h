@@ -48,6 +48,26 @@ cudaError_t allow_smem(F* kernel, int bytes, SmemRecord& have, bool large_cluste
   return e;
 }
 
+// A launch that may start while the kernel before it is ending (the kernels wait
+// for it themselves); cluster: CTAs of a cluster, or 0.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, int smem, cudaStream_t s, int cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct AppendParams {
   Cache c;
   const uint16_t* k;       // [B, n, H, D] bf16

@@ -76,13 +76,13 @@ __device__ __noinline__ uint32_t encode_key_f64(const uint16_t* row, const float
   double x[E], y[E], ss = 0., m = 0.;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    x[e] = (double)__uint_as_float((uint32_t)__ldg(row + lane * E + e) << 16);
+    x[e] = (double)__uint_as_float((uint32_t)*(row + lane * E + e) << 16);
     ss = fma(x[e], x[e], ss);
   }
   double sn[E], cs[E];
   if (ang != nullptr) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) sincos_f64((double)__ldg(ang + (lane & 15) * E + e), sn[e], cs[e]);
+    for (int e = 0; e < E; ++e) sincos_f64((double)*(ang + (lane & 15) * E + e), sn[e], cs[e]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -207,8 +207,10 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendParams
   using R = RowLanes<D>;
   const int lane = threadIdx.x & 31, li = lane % R::kLanes, sub = lane / R::kLanes;
   const int b = blockIdx.z, H = p.c.heads, cap = p.c.cap;
-  const int n = p.counts != nullptr ? min(max(__ldg(p.counts + b), 0), p.n) : p.n;
-  const int64_t start = __ldg(p.start + b);
+  let_next_start();
+  wait_for_previous();
+  const int n = p.counts != nullptr ? min(max(p.counts[b], 0), p.n) : p.n;
+  const int64_t start = p.start[b];
   if ((int)blockIdx.x < p.key_blocks * p.head_groups) {
     const int group = blockIdx.x / p.key_blocks;
     const int h0 = group * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, H);
@@ -303,7 +305,9 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadParams p) {
   constexpr int kLanes = D / 16;
   const int H = p.c.heads, cap = p.c.cap, b = blockIdx.z;
-  const int64_t start = p.start != nullptr ? (int64_t)__ldg(p.start + b) : 0;
+  let_next_start();
+  wait_for_previous();
+  const int64_t start = p.start != nullptr ? (int64_t)p.start[b] : 0;
   const int64_t first_row = start >= 0 ? start / 2 : -((1 - start) / 2);   // floor
   // items of a batch element: (row, head, lane), so that neighbours write neighbouring features
   const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -367,8 +371,7 @@ cudaError_t append_d(AppendParams p, cudaStream_t s) {
   p.heads_per_warp = kRope && (int64_t)p.key_blocks * p.c.batch >= 148 ? 8 : 1;
   p.head_groups = (p.c.heads + p.heads_per_warp - 1) / p.heads_per_warp;
   const dim3 grid(p.key_blocks * p.head_groups + value_blocks * p.c.heads, 1, p.c.batch);
-  kv4_append_kernel<D, kRope><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kv4_append_kernel<D, kRope>, grid, kThreads, 0, s, 0, p);
 }
 
 }  // namespace
@@ -381,9 +384,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
 cudaError_t launch_read(const ReadParams& p, cudaStream_t s) {
   const int64_t items = ((int64_t)p.n / 2 + 1) * p.c.heads * (p.c.dim / 16);
   const dim3 grid((unsigned)((items + kThreads - 1) / kThreads), 1, p.c.batch);
-  if (p.c.dim == 128) kv4_read_kernel<128><<<grid, kThreads, 0, s>>>(p);
-  else kv4_read_kernel<64><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(p.c.dim == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, grid, kThreads, 0, s, 0, p);
 }
 
 }  // namespace kv4

@@ -84,7 +84,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool o
 // token) or one value block (8 features of two tokens).
 template <int D, bool kValues, bool kLow>
 __global__ void __launch_bounds__(256, 3) kv4_expand_kernel(const FwdParams4 p, int fold_blocks) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   const int lane = threadIdx.x & 31;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
   const int BH = p.c.batch * p.c.heads;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(256, 3) kv4_expand_kernel(const FwdParams4 p, 
       const int hk = (int)(item % p.c.heads), i = (int)(item / p.c.heads % p.sq), b = (int)(item / p.c.heads / p.sq);
       float gain[16], sn[16], cs[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) gain[e] = qscale_of(p.gamma_q, p.gamma_k, p.scale_log2, li * 16 + e);
+      for (int e = 0; e < 16; ++e) gain[e] = query_gain(p, li * 16 + e);
       if (p.rope != nullptr) {
         float angles[16];
         load_angles<D>(p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2), li, angles);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256, 3) kv4_expand_kernel(const FwdParams4 p, 
   const int64_t items = (int64_t)BH * tiles;
   for (int64_t it = (int64_t)blockIdx.x - fold_blocks; it < items; it += (int64_t)gridDim.x - fold_blocks) {
     const int bh = (int)(it / tiles), tile = (int)(it % tiles);
-    const int len = min(max(__ldg(p.lengths + bh / p.c.heads), 0), p.c.cap);
+    const int len = min(max(p.lengths[bh / p.c.heads], 0), p.c.cap);
     if (tile * 128 >= len) continue;
     const int64_t tok0 = (int64_t)bh * p.c.cap + tile * 128;
     // a thread's key and value blocks of the tile, all loads before the first store
@@ -170,12 +170,12 @@ __global__ void __launch_bounds__(256, 3) kv4_expand_kernel(const FwdParams4 p, 
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       const int i = n * 256 + threadIdx.x;
-      kw[n] = __ldg(reinterpret_cast<const uint2*>(p.c.kc + tok0 * (D / 2)) + i);
-      ks[n] = __ldg(p.c.ks + tok0 * (D / 16) + i);
+      kw[n] = *(reinterpret_cast<const uint2*>(p.c.kc + tok0 * (D / 2)) + i);
+      ks[n] = *(p.c.ks + tok0 * (D / 16) + i);
       if constexpr (kValues) {
         const int pr = i / (D / 8), f = i % (D / 8) * 8;   // row of two tokens, first of 8 features
-        vw[n] = __ldg(reinterpret_cast<const uint2*>(p.c.vc + (tok0 / 2 + pr) * D + f));
-        vs[n] = __ldg(reinterpret_cast<const uint16_t*>(p.c.vs + ((tok0 / 2 + pr) * (D / 16) + f / 16) * 2));
+        vw[n] = *(reinterpret_cast<const uint2*>(p.c.vc + (tok0 / 2 + pr) * D + f));
+        vs[n] = *(reinterpret_cast<const uint16_t*>(p.c.vs + ((tok0 / 2 + pr) * (D / 16) + f / 16) * 2));
       }
     }
 #pragma unroll
@@ -236,7 +236,7 @@ struct FwdBars {
 
 // ---- units: pairs of row tiles, numbered by batch element, head and pair
 __device__ __forceinline__ int tiles_of(const FwdParams4& p, int b) {
-  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  const int len = min(max(p.lengths[b], 0), p.c.cap);
   return (len + 127) / 128;
 }
 
@@ -282,7 +282,7 @@ __device__ __forceinline__ bool next_piece(const FwdParams4& p, Walk& w, Piece& 
       u = (int)blockIdx.x + w.round * (int)gridDim.x;
       ++w.round;
       o.b = u / w.per;
-      o.len = min(max(__ldg(p.lengths + o.b), 0), p.c.cap);
+      o.len = min(max(p.lengths[o.b], 0), p.c.cap);
       tiles = (o.len + 127) / 128;
       if (tiles == 0) continue;
       o.t_begin = 0;
@@ -292,7 +292,7 @@ __device__ __forceinline__ bool next_piece(const FwdParams4& p, Walk& w, Piece& 
     if (w.x >= w.x1) return false;
     u = w.u;
     o.b = u / w.per;
-    o.len = min(max(__ldg(p.lengths + o.b), 0), p.c.cap);
+    o.len = min(max(p.lengths[o.b], 0), p.c.cap);
     tiles = (o.len + 127) / 128;
     if (w.x >= w.begin + tiles) {   // past this unit
       w.begin += tiles;
@@ -341,7 +341,8 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   walk.rounds = p.c.batch * walk.per / (int)gridDim.x;
   walk.u0 = walk.rounds * (int)gridDim.x;
 
-  // batch elements without a key: their rows are the base part's, or empty
+  // batch elements without a key: their rows are the base part's, or empty.
+  // (The lengths and the base part were there before the expansion started.)
   for (int b = 0; b < p.c.batch; ++b) {
     if (tiles_of(p, b) > 0) continue;
     float zero[32] = {};
@@ -401,8 +402,8 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the expansion
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();   // the expansion
+  let_next_start();
   walk.x = part->x;
   walk.x1 = part->y;
   walk.u = part->z;
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(256) kv4_chunk_combine_kernel(const FwdParams4
   int below, all;
   tiles_below(p, u0, per, b, lane, below, all);
   const int tiles = tiles_of(p, b);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   if (row >= rows || tiles == 0) return;   // no keys: finished where that was seen
   const Parts<4> parts(all, ctas);
   const int x0 = below + (u - max(u0, b * per)) * tiles;
@@ -744,9 +745,9 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x * 2, bh = blockIdx.y, split = blockIdx.z;
   const int b = bh / p.c.heads;
-  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  const int len = min(max(p.lengths[b], 0), p.c.cap);
   if (tile * 128 >= len) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     return;
   }
   const int n_kt = (tile + 1) * 128 < len ? 2 : 1;   // key tiles
@@ -784,7 +785,7 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the expansion
+  wait_for_previous();   // the expansion
 
   if (warp == 9) {
     if (elect_one()) {
@@ -922,30 +923,14 @@ kv4_chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_qh, const __grid
 
 // Joins the parts of the weights, in their order.
 __global__ void __launch_bounds__(256) kv4_weights_sum_kernel(const FwdParams4 p) {
+  wait_for_previous();
   const int bh = blockIdx.y, at = blockIdx.x * 256 + threadIdx.x;
-  const int len = min(max(__ldg(p.lengths + bh / p.c.heads), 0), p.c.cap);
+  const int len = min(max(p.lengths[bh / p.c.heads], 0), p.c.cap);
   if (at >= len) return;
   const int64_t i = (int64_t)bh * p.c.cap + at, stride = (int64_t)p.c.batch * p.c.heads * p.c.cap;
   float x = 0.f;
   for (int s = 0; s < p.n_splits; ++s) x += p.part_o[s * stride + i];
   p.weights[i] = p.decay != 0.f ? fmaf(p.decay, p.weights[i], x) : x;
-}
-
-// A launch that may start while the kernel before it is ending (the kernels wait
-// for it themselves).
-template <typename... Args>
-cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int block, int smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Units of the attention, and the CTAs that take them: one an SM, fewer only if
@@ -974,10 +959,10 @@ cudaError_t chunk_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   if (e != cudaSuccess) return e;
   const int rows = p.heads_q / p.c.heads * p.sq;
   const int units = chunk_units(p.c, rows), ctas = chunk_ctas(p.c, rows);
-  e = launch_early(kv4_chunk_fwd_kernel<D>, dim3(ctas), kThreads, FwdLayout<D>::kAlloc, s, tq, tk, tv, p);
+  e = launch_early(kv4_chunk_fwd_kernel<D>, dim3(ctas), kThreads, FwdLayout<D>::kAlloc, s, 0, tq, tk, tv, p);
   const int u0 = units / ctas * ctas;
   if (e != cudaSuccess || u0 == units) return e;
-  return launch_early(kv4_chunk_combine_kernel<D>, dim3(8, units - u0), 256, 0, s, p, u0, ctas);
+  return launch_early(kv4_chunk_combine_kernel<D>, dim3(8, units - u0), 256, 0, s, 0, p, u0, ctas);
 }
 
 template <int D>
@@ -987,11 +972,10 @@ cudaError_t chunk_weights_d(const CUtensorMap& tqh, const CUtensorMap& tql, cons
   cudaError_t e = allow_smem(kv4_chunk_weights_kernel<D>, WLayout<D>::kAlloc, have);
   if (e != cudaSuccess) return e;
   const int BH = p.c.batch * p.c.heads;
-  e = launch_early(kv4_chunk_weights_kernel<D>, dim3((p.c.cap + 255) / 256, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s, tqh,
-                   tql, tk, p);
+  e = launch_early(kv4_chunk_weights_kernel<D>, dim3((p.c.cap + 255) / 256, BH, p.n_splits), kThreads, WLayout<D>::kAlloc, s, 0,
+                   tqh, tql, tk, p);
   if (e != cudaSuccess || p.n_splits == 1) return e;
-  kv4_weights_sum_kernel<<<dim3((p.c.cap + 255) / 256, BH), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kv4_weights_sum_kernel, dim3((p.c.cap + 255) / 256, BH), 256, 0, s, 0, p);
 }
 
 }  // namespace

@@ -64,7 +64,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.y, b = bh / p.src.heads;
-  const int len = min(max(__ldg(p.lengths + b), 0), p.src.cap);
+  let_next_start();
+  wait_for_previous();
+  const int len = min(max(p.lengths[b], 0), p.src.cap);
   const int kept = min(len, p.keep);
   const int rec = min(p.recent, kept);
   const int n = len - rec;                      // candidates [0, n)
@@ -80,7 +82,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   // the keys of four neighbours; 0, which no weight has, behind the last (the
   // row has 128-slot granularity, so reading four is always inside it)
   auto from_row = [&](int o) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(w + a0 + o));
+    const float4 x = *(reinterpret_cast<const float4*>(w + a0 + o));
     return make_uint4(order_key(x.x), o + 1 < len_w ? order_key(x.y) : 0u, o + 2 < len_w ? order_key(x.z) : 0u,
                       o + 3 < len_w ? order_key(x.w) : 0u);
   };
@@ -219,29 +221,30 @@ __global__ void __launch_bounds__(256) kv4_move_kernel(const EvictParams p) {
   constexpr int kTok = 16;
   constexpr int kK = D / 32;       // 16-byte pieces of a key row
   constexpr int kV = D / 16;       // 16-byte pieces of a value row (two tokens)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / p.src.heads;
-  const int kept = min(min(max(__ldg(p.lengths + b), 0), p.src.cap), p.keep);
+  const int kept = min(min(max(p.lengths[b], 0), p.src.cap), p.keep);
   const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kTok;
   const int n = min(kTok, kept - t0);
   if (n <= 0) return;
   const int64_t src = (int64_t)bh * p.src.cap, dst = (int64_t)bh * p.dst.cap + t0;
   // lane t (and t + 16): where token t of the sixteen comes from
-  const int from = p.index[(int64_t)bh * p.keep + t0 + min(lane & 15, n - 1)];   // not __ldg: written while this grid was starting
+  const int from = p.index[(int64_t)bh * p.keep + t0 + min(lane & 15, n - 1)];
   uint4 k[kK * kTok / 32], va[kV * kTok / 64], vb[kV * kTok / 64];
 #pragma unroll
   for (int i = 0; i < kK * kTok / 32; ++i) {
     const int piece = i * 32 + lane, t = piece / kK;
     const int s = __shfl_sync(0xffffffffu, from, t);
-    k[i] = __ldg(reinterpret_cast<const uint4*>(p.src.kc + (src + s) * (D / 2)) + piece % kK);
+    k[i] = *(reinterpret_cast<const uint4*>(p.src.kc + (src + s) * (D / 2)) + piece % kK);
   }
 #pragma unroll
   for (int i = 0; i < kV * kTok / 64; ++i) {
     const int piece = i * 32 + lane, r = piece / kV;
     const int s0 = __shfl_sync(0xffffffffu, from, 2 * r), s1 = __shfl_sync(0xffffffffu, from, 2 * r + 1);
-    va[i] = __ldg(reinterpret_cast<const uint4*>(p.src.vc + (src / 2 + s0 / 2) * D) + piece % kV);
-    vb[i] = __ldg(reinterpret_cast<const uint4*>(p.src.vc + (src / 2 + s1 / 2) * D) + piece % kV);
+    va[i] = *(reinterpret_cast<const uint4*>(p.src.vc + (src / 2 + s0 / 2) * D) + piece % kV);
+    vb[i] = *(reinterpret_cast<const uint4*>(p.src.vc + (src / 2 + s1 / 2) * D) + piece % kV);
   }
   // scales: lanes 0..15 a token's key and value scales each; lane t + 16 its weight
   uint2 ks = make_uint2(0, 0);
@@ -249,16 +252,16 @@ __global__ void __launch_bounds__(256) kv4_move_kernel(const EvictParams p) {
   float w = 0.f;
   if (lane < 16) {
     if constexpr (D == 128) {
-      ks = __ldg(reinterpret_cast<const uint2*>(p.src.ks + (src + from) * 8));
-      vs = __ldg(reinterpret_cast<const uint4*>(p.src.vs + (src / 2 + from / 2) * 16));
+      ks = *(reinterpret_cast<const uint2*>(p.src.ks + (src + from) * 8));
+      vs = *(reinterpret_cast<const uint4*>(p.src.vs + (src / 2 + from / 2) * 16));
     } else {
-      ks.x = __ldg(reinterpret_cast<const uint32_t*>(p.src.ks + (src + from) * 4));
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(p.src.vs + (src / 2 + from / 2) * 8));
+      ks.x = *(reinterpret_cast<const uint32_t*>(p.src.ks + (src + from) * 4));
+      const uint2 y = *(reinterpret_cast<const uint2*>(p.src.vs + (src / 2 + from / 2) * 8));
       vs.x = y.x;
       vs.y = y.y;
     }
   } else {
-    w = __ldg(p.w_src + src + from);
+    w = *(p.w_src + src + from);
   }
 
 #pragma unroll
@@ -306,21 +309,11 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   static SmemRecord have;
   cudaError_t e = allow_smem(kv4_select_kernel, bytes, have);
   if (e != cudaSuccess) return e;
-  kv4_select_kernel<<<dim3(kCluster, BH), kSelThreads, bytes, s>>>(p, held);
-  e = cudaGetLastError();
+  e = launch_early(kv4_select_kernel, dim3(kCluster, BH), kSelThreads, bytes, s, 0, p, held);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   const int most = std::min(p.keep, p.src.cap);
-  cfg.gridDim = dim3((unsigned)((most + 127) / 128), (unsigned)BH);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return p.src.dim == 128 ? cudaLaunchKernelEx(&cfg, kv4_move_kernel<128>, p)
-                          : cudaLaunchKernelEx(&cfg, kv4_move_kernel<64>, p);
+  return launch_early(p.src.dim == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>,
+                      dim3((unsigned)((most + 127) / 128), (unsigned)BH), 256, 0, s, 0, p);
 }
 
 }  // namespace kv4

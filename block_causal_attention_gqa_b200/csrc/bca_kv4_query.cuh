@@ -16,6 +16,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// gamma_q gamma_k scale log2(e) of feature d.
+__device__ __forceinline__ float query_gain(const FwdParams4& p, int d) { return p.gamma_q[d] * p.gamma_k[d] * p.scale_log2; }
+
 // Row `row` of (b, hk)'s rows (group head g = row / Sq, query row % Sq), folded,
 // by one warp: lane holds features [lane*E, lane*E + E), E = D/32, as fp16
 // pairs hi and what they leave, lo.  A row behind the last is zero.
@@ -28,21 +31,26 @@ __device__ __forceinline__ void fold_query(const FwdParams4& p, int b, int hk, i
     const int h = hk * G + row / p.sq, i = row % p.sq;
     const uint16_t* src = p.q + (((int64_t)b * p.sq + i) * p.heads_q + h) * D + lane * E;
     if constexpr (E == 4) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+      const uint2 w = *(reinterpret_cast<const uint2*>(src));
       x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
     } else {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src));
+      const uint32_t w = *(reinterpret_cast<const uint32_t*>(src));
       x[0] = bf16_lo(w); x[1] = bf16_hi(w);
     }
     const float r = rms_inv<D>(warp_sumsq_row<E>(x), p.eps);
     if (p.rope != nullptr) {
-      float y[E];
-      rope_warp<D>(x, p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2), lane, y);
+      // the pair of feature d is d +- D/2, half the warp away
+      const float* ang = p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2) + (lane & 15) * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = y[e];
+      for (int e = 0; e < E; ++e) {
+        const float o = __shfl_xor_sync(0xffffffffu, x[e], 16);
+        float sn, cs;
+        sincosf(ang[e], &sn, &cs);
+        x[e] = lane < 16 ? rope_first(x[e], o, cs, sn) : rope_second(o, x[e], cs, sn);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = x[e] * r * qscale_of(p.gamma_q, p.gamma_k, p.scale_log2, lane * E + e);
+    for (int e = 0; e < E; ++e) x[e] = x[e] * r * query_gain(p, lane * E + e);
   }
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
@@ -77,15 +85,15 @@ __device__ __forceinline__ void load_words(const uint16_t* src, uint32_t (&w)[N]
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i / 4);
+      const uint4 x = *(reinterpret_cast<const uint4*>(src) + i / 4);
       w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
     }
   } else if constexpr (N == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+    const uint2 x = *(reinterpret_cast<const uint2*>(src));
     w[0] = x.x; w[1] = x.y;
   } else {
     static_assert(N == 1, "1, 2 or a multiple of 4 words");
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    w[0] = *(reinterpret_cast<const uint32_t*>(src));
   }
 }
 
@@ -125,7 +133,7 @@ __device__ __forceinline__ void finish_row(const FwdParams4& p, int b, int hk, i
   float lse = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
   float scale = m == -INFINITY ? 0.f : 1.f / l;
   if (p.base_out != nullptr) {
-    const float base = __ldg(p.base_lse + at_lse);
+    const float base = *(p.base_lse + at_lse);
     const float top = fmaxf(lse, base);
     if (!(lse == -INFINITY && base == -INFINITY)) {
       const float a = expf(lse - top), e = expf(base - top);

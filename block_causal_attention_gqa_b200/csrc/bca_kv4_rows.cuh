@@ -92,7 +92,7 @@ struct RowLanes {
 __device__ __forceinline__ void load_block(const uint16_t* src, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    const uint4 w = *(reinterpret_cast<const uint4*>(src) + i);
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -108,7 +108,7 @@ __device__ __forceinline__ void load_angles(const float* row, int li, float (&a)
   const float4* src = reinterpret_cast<const float4*>(row + li % (D / 32) * 16);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(src + i);
+    const float4 v = *(src + i);
     a[4 * i] = v.x; a[4 * i + 1] = v.y; a[4 * i + 2] = v.z; a[4 * i + 3] = v.w;
   }
 }

@@ -39,7 +39,7 @@
 // histories of any number and lengths keep every SM busy to the end.  A part of
 // one history is a piece; piece (CTA c, history h) has slot c + h of the
 // workspace, which no other has.  kv4_combine_kernel joins the pieces' (m, l,
-// O), launched early by programmatic dependent launch.
+// O).
 //
 // Short histories (token_cluster() says which) are a matter of latency: there a
 // cluster of up to 16 CTAs takes a history, joins its parts through
@@ -167,7 +167,7 @@ __device__ __forceinline__ void load_query_fragments(const uint8_t* smem_q, int 
 //
 // All in 32 bits: token_steps_fit() has checked the totals.
 __device__ __forceinline__ int steps_of(const FwdParams4& p, int b) {
-  const int len = min(max(__ldg(p.lengths + b), 0), p.c.cap);
+  const int len = min(max(p.lengths[b], 0), p.c.cap);
   return (len + kStep - 1) / kStep;
 }
 
@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     fence_mbar_init();
   }
   __syncwarp();
+  if constexpr (kCluster) let_next_start();
+  wait_for_previous();
   // every warp for itself: the lengths come from the cache, and no one waits
   int4 part;
   int rank = 0, size = 1;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
 
   // one piece: steps [s_begin, s_end) of one history (a cluster's CTA without steps still joins)
   for (bool first = kCluster; x < x1 || first; first = false) {
-    const int len = uniform(min(max(__ldg(p.lengths + b), 0), p.c.cap));
+    const int len = uniform(min(max(p.lengths[b], 0), p.c.cap));
     const int steps = (len + kStep - 1) / kStep;
     if (!kCluster && (steps == 0 || x >= begin + steps * per)) {   // on to the next batch element
       begin += steps * per;
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
       }
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
 }
 
 // Joins the pieces of the rows: one CTA a row, its warps every eighth piece.
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(256) kv4_token_combine_kernel(const FwdParams4
     slot = ((int64_t)b * per + hist + c0) * kRows + row % kRows;
     n = parts.of(x0 + steps - 1) - c0 + 1;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   float mm = -INFINITY, ll = 0.f;
   float acc[F] = {};
   for (int s0 = warp; s0 < n; s0 += 4 * W) {   // four pieces at a time
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_token_weights_kernel(const Fw
   const bool add = p.decay != 0.f;   // a factor of 0 replaces the weights, whatever they hold
 
   while (x < x1) {
-    const int len = uniform(min(max(__ldg(p.lengths + b), 0), p.c.cap));
+    const int len = uniform(min(max(p.lengths[b], 0), p.c.cap));
     const int steps = (len + kStep - 1) / kStep;
     if (steps == 0 || x >= begin + steps * p.c.heads) {
       begin += steps * p.c.heads;
@@ -771,23 +773,13 @@ template <int D, int NT>
 static cudaError_t token_fwd_d(const FwdParams4& p, cudaStream_t s) {
   using R = Ring<D, NT>;
   const int rows = p.heads_q / p.c.heads * p.sq;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at;
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
   const int cluster = token_cluster(p.c, rows);
   if (cluster > 0) {
     static SmemRecord have;
-    cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, true>, R::kTotal, have, true);
+    const cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, true>, R::kTotal, have, true);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(histories(p.c, rows, false) * cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = R::kTotal;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_token_fwd_kernel<D, NT, true>, p);
+    return launch_early(kv4_token_fwd_kernel<D, NT, true>, dim3((unsigned)(histories(p.c, rows, false) * cluster)), kThreads,
+                        R::kTotal, s, cluster, p);
   }
   static SmemRecord have;
   cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, false>, R::kTotal, have);
@@ -796,11 +788,8 @@ static cudaError_t token_fwd_d(const FwdParams4& p, cudaStream_t s) {
   kv4_token_fwd_kernel<D, NT, false><<<ctas, kThreads, R::kTotal, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((int64_t)p.c.batch * p.heads_q * p.sq));
-  cfg.blockDim = dim3(256);
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_token_combine_kernel<D>, p, 4 * NT, ctas);
+  return launch_early(kv4_token_combine_kernel<D>, dim3((unsigned)((int64_t)p.c.batch * p.heads_q * p.sq)), 256, 0, s, 0, p,
+                      4 * NT, ctas);
 }
 
 cudaError_t launch_token_fwd(const FwdParams4& p, cudaStream_t s) {
