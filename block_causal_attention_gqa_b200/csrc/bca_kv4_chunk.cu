@@ -313,14 +313,15 @@ __device__ __forceinline__ bool next_piece(const FwdParams4& p, Walk& w, Piece& 
   return true;
 }
 
+// A piece's row, 32 features from f0: [slot][quad of features][row], so that the
+// rows of a warp's lanes are neighbours.
 template <int D>
 __device__ __forceinline__ void write_piece(const FwdParams4& p, int slot, int row, int f0, float m, float l,
                                             const float (&o)[32]) {
-  const int64_t at = (int64_t)slot * 256 + row;
-  if (f0 == 0) p.part_ml[at] = make_float2(m, l);
+  if (f0 == 0) p.part_ml[(int64_t)slot * 256 + row] = make_float2(m, l);
+  float4* dst = reinterpret_cast<float4*>(p.part_o) + ((int64_t)slot * (D / 4) + f0 / 4) * 256 + row;
 #pragma unroll
-  for (int f = 0; f < 32; f += 4)
-    *reinterpret_cast<float4*>(p.part_o + at * D + f0 + f) = make_float4(o[f], o[f + 1], o[f + 2], o[f + 3]);
+  for (int f = 0; f < 32; f += 4) dst[f / 4 * 256] = make_float4(o[f], o[f + 1], o[f + 2], o[f + 3]);
 }
 
 template <int D>
@@ -662,56 +663,59 @@ kv4_chunk_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
-// Joins the pieces of the units from u0 on that were cut: a warp takes four
-// rows, whose loads are under way together.
+// Joins the pieces of the units from u0 on that were cut: a CTA takes 32 rows, a
+// lane one of them and a warp every eighth quad of features (as the pieces lie),
+// and turns them in shared memory into rows.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_chunk_combine_kernel(const FwdParams4 p, int u0, int ctas) {
-  constexpr int F = D / 32, kR = 4;
-  const int lane = threadIdx.x & 31;
+  constexpr int F = D / 32;
+  __shared__ float so[32][D + 4];
+  __shared__ float2 sml[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
   const int pairs = (rows + 255) / 256, per = p.c.heads * pairs;
   const int u = u0 + (int)blockIdx.y, b = u / per, rem = u - b * per, hk = rem / pairs;
-  const int r = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * kR, row = (rem - hk * pairs) * 256 + r;
+  const int r0 = (int)blockIdx.x * 32, row0 = (rem - hk * pairs) * 256 + r0;
   int below, all;
   tiles_below(p, u0, per, b, lane, below, all);
   const int tiles = tiles_of(p, b);
   wait_for_previous();
-  if (row >= rows || tiles == 0) return;   // no keys: finished where that was seen
+  if (row0 >= rows || tiles == 0) return;  // no keys: finished where that was seen
   const Parts<4> parts(all, ctas);
   const int x0 = below + (u - max(u0, b * per)) * tiles;
   const int c0 = parts.of(x0), n = parts.of(x0 + tiles - 1) - c0 + 1;
   if (n == 1) return;                      // not cut
-  const int64_t at0 = (int64_t)(c0 + u - u0) * 256 + r;   // piece i: 256 rows on
-  float mm[kR], ll[kR], acc[kR][F];
+  const int64_t slot = c0 + u - u0;        // piece i: slot + i
+  const float2* ml = p.part_ml + slot * 256 + r0 + lane;
+  float mm = ml[0].x, ll = 0.f;            // every piece has a key, so the references are finite (or NaN)
+  for (int i = 1; i < n; ++i) mm = fmaxf(mm, ml[i * 256].x);
+  const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (D / 4) + warp) * 256 + r0 + lane;
+  float4 acc[D / 32] = {};
+  for (int i = 0; i < n; ++i) {
+    const float2 x = ml[i * 256];
+    const float w = fast_exp2(x.x - mm);
+    ll = fmaf(x.y, w, ll);
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
-    const float2 ml = p.part_ml[at0 + k];
-    mm[k] = ml.x;
-    ll[k] = ml.y;
-    load_floats<F>(p.part_o + (at0 + k) * D + lane * F, acc[k]);
-  }
-  for (int i = 1; i < n; ++i) {
-    float2 ml[kR];
-    float o[kR][F];
-#pragma unroll
-    for (int k = 0; k < kR; ++k) {
-      const int64_t at = at0 + (int64_t)i * 256 + k;
-      ml[k] = p.part_ml[at];
-      load_floats<F>(p.part_o + at * D + lane * F, o[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kR; ++k) {         // every piece has a key, so the references are finite
-      const float m1 = fmaxf(mm[k], ml[k].x);
-      const float w0 = fast_exp2(mm[k] - m1), w1 = fast_exp2(ml[k].x - m1);
-      mm[k] = m1;
-      ll[k] = fmaf(ml[k].y, w1, ll[k] * w0);
-#pragma unroll
-      for (int f = 0; f < F; ++f) acc[k][f] = fmaf(o[k][f], w1, acc[k][f] * w0);
+    for (int k = 0; k < D / 32; ++k) {
+      const float4 v = src[((int64_t)i * (D / 4) + k * 8) * 256];
+      acc[k].x = fmaf(v.x, w, acc[k].x);
+      acc[k].y = fmaf(v.y, w, acc[k].y);
+      acc[k].z = fmaf(v.z, w, acc[k].z);
+      acc[k].w = fmaf(v.w, w, acc[k].w);
     }
   }
 #pragma unroll
-  for (int k = 0; k < kR; ++k)
-    if (row + k < rows) finish_row<F>(p, b, hk, G, row + k, D, lane * F, mm[k], ll[k], acc[k]);
+  for (int k = 0; k < D / 32; ++k) *reinterpret_cast<float4*>(&so[lane][(warp + k * 8) * 4]) = acc[k];
+  if (warp == 0) sml[lane] = make_float2(mm, ll);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = warp * 4 + k;
+    float o[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) o[f] = so[r][lane * F + f];
+    if (row0 + r < rows) finish_row<F>(p, b, hk, G, row0 + r, D, lane * F, sml[r].x, sml[r].y, o);
+  }
 }
 
 // ------------------------------------------------------------------ weights

@@ -98,18 +98,6 @@ __device__ __forceinline__ void load_words(const uint16_t* src, uint32_t (&w)[N]
 }
 
 template <int N>
-__device__ __forceinline__ void load_floats(const float* src, float (&x)[N]) {
-  if constexpr (N == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(src);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else {
-    static_assert(N == 2, "2 or 4 floats");
-    const float2 v = *reinterpret_cast<const float2*>(src);
-    x[0] = v.x; x[1] = v.y;
-  }
-}
-
-template <int N>
 __device__ __forceinline__ void store_words(uint16_t* dst, const uint32_t (&w)[N]) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
