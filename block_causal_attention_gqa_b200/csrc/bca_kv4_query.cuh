@@ -2,7 +2,7 @@
 //   Q^ = rot(q) r_q gamma_q gamma_k scale log2(e)
 // as two fp16 numbers, and the last step of a row.
 #pragma once
-#include "bca_kv4.cuh"
+#include "bca_kv4_rows.cuh"
 
 namespace magi {
 namespace kv4 {
@@ -37,20 +37,25 @@ __device__ __forceinline__ void fold_query(const FwdParams4& p, int b, int hk, i
       const uint32_t w = *(reinterpret_cast<const uint32_t*>(src));
       x[0] = bf16_lo(w); x[1] = bf16_hi(w);
     }
+    float gain[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) gain[e] = query_gain(p, lane * E + e);
     const float r = rms_inv<D>(warp_sumsq_row<E>(x), p.eps);
     if (p.rope != nullptr) {
       // the pair of feature d is d +- D/2, half the warp away
       const float* ang = p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2) + (lane & 15) * E;
+      float a[E], sn[E], cs[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = ang[e];
+      sincos_row<E>(a, sn, cs);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float o = __shfl_xor_sync(0xffffffffu, x[e], 16);
-        float sn, cs;
-        sincosf(ang[e], &sn, &cs);
-        x[e] = lane < 16 ? rope_first(x[e], o, cs, sn) : rope_second(o, x[e], cs, sn);
+        x[e] = lane < 16 ? rope_first(x[e], o, cs[e], sn[e]) : rope_second(o, x[e], cs[e], sn[e]);
       }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = x[e] * r * query_gain(p, lane * E + e);
+    for (int e = 0; e < E; ++e) x[e] = x[e] * r * gain[e];
   }
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
