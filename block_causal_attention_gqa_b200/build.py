@@ -1,4 +1,5 @@
-"""Builds libmagi_bca.so in-tree with nvcc for sm_100a.
+"""Builds libmagi_bca.so in-tree with nvcc for sm_100a, and _kv4_binding.so, the
+cache's Python binding, with the host compiler against torch's headers.
 
 Usage: python -m block_causal_attention_gqa_b200.build [-v] [--debug]
 
@@ -8,15 +9,18 @@ unit is out of range, records a device status code (read as
 MAGI_BCA_DEVICE_CHECK) and returns before touching memory.  The binding loads
 it when MAGI_BCA_LIBRARY names its path.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmagi_bca.so")
 DEBUG_LIB = os.path.join(HERE, "libmagi_bca_debug.so")
+BINDING = os.path.join(HERE, "_kv4_binding.so")
 SOURCES = ["bca_api.cu", "bca_fwd.cu", "bca_bwd.cu", "bca_bwd_split.cu", "bca_noalloc.cu", "bca_sched.cpp",
            "bca_kv4_api.cu", "bca_kv4_append.cu", "bca_kv4_token.cu", "bca_kv4_chunk.cu", "bca_kv4_evict.cu"]
 DEPS = SOURCES + ["sm100.cuh", "bca_kernels.h", "bca_sched.h", "bca_norm.cuh", "bca_bwd_common.cuh", "bca_mask.cuh",
@@ -30,15 +34,32 @@ def nvcc():
     return "nvcc"
 
 
-def needs_build(lib=LIB):
+def needs_build(lib=LIB, deps=DEPS):
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    paths = [os.path.join(CSRC, f) for f in DEPS] + [os.path.join(ROOT, "include", "magi_bca.h"), __file__]
+    paths = [os.path.join(CSRC, f) for f in deps] + [os.path.join(ROOT, "include", "magi_bca.h"), __file__]
     return any(os.path.getmtime(p) > t for p in paths if os.path.exists(p))
 
 
+def build_binding(force=False):
+    if not force and not needs_build(BINDING, ["kv4_binding.cpp"]):
+        return BINDING
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    include = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    # the compiler that nvcc uses too: a C++ runtime of the binding's own (as some
+    # wrappers link in) does not go with torch's
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + i for i in include),
+           "-o", BINDING, os.path.join(CSRC, "kv4_binding.cpp"), "-L" + os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+    subprocess.run(cmd, check=True)
+    return BINDING
+
+
 def build(force=False, verbose=False, debug=False):
+    build_binding(force)
     lib = DEBUG_LIB if debug else LIB
     if not force and not needs_build(lib):
         return lib

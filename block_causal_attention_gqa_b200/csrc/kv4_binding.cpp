@@ -1,0 +1,432 @@
+// Python side of the magi_bca_kv4_* entry points: checks the tensors, makes
+// outputs and workspaces and passes addresses on.
+//
+// A step of decoding is some microseconds of device time, and the same work in
+// Python (a handful of attributes of each of a dozen tensors) took longer than
+// the kernels: 15.0 us for an attention of one token whose kernel takes 7.6.
+// Here a tensor's checks are some ten nanoseconds.  kv4.py keeps the public
+// functions with their defaults and documentation; it passes every argument by
+// position, and the addresses of the entry points once (bind).
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <array>
+#include <limits>
+#include <optional>
+#include <string>
+
+#include "../../include/magi_bca.h"
+
+namespace {
+
+struct Refused {};   // the Python error is set
+
+[[noreturn]] void refuse(PyObject* type, const std::string& text) {
+  PyErr_SetString(type, text.c_str());
+  throw Refused{};
+}
+
+// The entry points and the function that makes the error of a status.
+struct Entry {
+  decltype(&magi_bca_kv4_append) append;
+  decltype(&magi_bca_kv4_read) read;
+  decltype(&magi_bca_kv4_fwd) fwd;
+  decltype(&magi_bca_kv4_weights) weights;
+  decltype(&magi_bca_kv4_evict) evict;
+  decltype(&magi_bca_kv4_fwd_workspace_size) fwd_size;
+  decltype(&magi_bca_kv4_weights_workspace_size) weights_size;
+  PyObject* error;
+} g_entry;
+
+std::string text_of(at::IntArrayRef shape) {
+  std::string s = "(";
+  for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
+  return s + (shape.size() == 1 ? ",)" : ")");
+}
+
+const char* text_of(at::ScalarType t) {
+  return t == at::kByte ? "uint8" : t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : "int32";
+}
+
+const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+// The tensor's address, if it is a contiguous one of this type and shape on device `dev`.
+void* check(const char* name, const at::Tensor* t, at::ScalarType type, at::IntArrayRef shape, int dev, const char* of = "") {
+  if (t == nullptr || t->scalar_type() != type || !t->is_cuda() || !t->is_contiguous())
+    refuse(PyExc_TypeError, std::string(of) + name + " must be a contiguous " + text_of(type) + " CUDA tensor");
+  if (t->sizes() != shape)
+    refuse(PyExc_ValueError, std::string(of) + name + " has shape " + text_of(t->sizes()) + ", expected " + text_of(shape));
+  if (t->get_device() != dev)
+    refuse(PyExc_ValueError,
+           std::string(of) + name + " is on " + t->device().str() + ", the call runs on cuda:" + std::to_string(dev));
+  return t->data_ptr();
+}
+template <typename T>
+T* check(const char* name, PyObject* o, at::ScalarType type, at::IntArrayRef shape, int dev) {
+  return static_cast<T*>(check(name, tensor(o), type, shape, dev));
+}
+
+int32_t int32_of(const char* name, int64_t v) {
+  if (v > std::numeric_limits<int32_t>::max() || v < std::numeric_limits<int32_t>::min())
+    refuse(PyExc_ValueError, std::string(name) + " is out of range");
+  return (int32_t)v;
+}
+int32_t int_arg(const char* name, PyObject* o) {
+  PyObject* n = PyNumber_Long(o);
+  if (n == nullptr) throw Refused{};
+  int overflow = 0;
+  const long long v = PyLong_AsLongLongAndOverflow(n, &overflow);
+  Py_DECREF(n);
+  if (overflow != 0) refuse(PyExc_ValueError, std::string(name) + " is out of range");
+  if (v == -1 && PyErr_Occurred()) throw Refused{};
+  return int32_of(name, v);
+}
+float float_arg(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+  return (float)v;
+}
+
+// The device a call runs on is that of its first tensor, which has 4 dimensions.
+const at::Tensor& first(const char* name, const at::Tensor* t) {
+  if (t == nullptr || !t->is_cuda()) refuse(PyExc_TypeError, std::string(name) + " must be a CUDA tensor");
+  if (t->dim() != 4)
+    refuse(PyExc_ValueError, std::string(name) + " has shape " + text_of(t->sizes()) + ", expected 4 dimensions");
+  return *t;
+}
+const at::Tensor& first(const char* name, PyObject* o) { return first(name, tensor(o)); }
+
+// A cache is any sequence of its four tensors.
+struct CacheArg {
+  std::array<const at::Tensor*, 4> t;
+  magi_bca_kv4_cache c;
+  int64_t B, H, D, cap;
+
+  explicit CacheArg(PyObject* o) {
+    PyObject* seq = PySequence_Fast(o, "a cache is its four tensors: k_codes, k_scales, v_codes, v_scales");
+    if (seq == nullptr) throw Refused{};
+    const bool four = PySequence_Fast_GET_SIZE(seq) == 4;
+    if (four)   // the caller's object keeps the tensors alive
+      for (int i = 0; i < 4; ++i) t[i] = tensor(PySequence_Fast_GET_ITEM(seq, i));
+    hold = seq;
+    if (!four) {
+      Py_DECREF(seq);
+      refuse(PyExc_ValueError, "a cache is its four tensors: k_codes, k_scales, v_codes, v_scales");
+    }
+  }
+  ~CacheArg() { Py_DECREF(hold); }
+  CacheArg(const CacheArg&) = delete;
+  CacheArg& operator=(const CacheArg&) = delete;
+
+  void look(int dev, const char* of = "cache.") {
+    if (t[0] == nullptr || t[0]->dim() != 4)
+      refuse(PyExc_TypeError, std::string(of) + "k_codes must be a uint8 CUDA tensor [batch, heads_kv, capacity, head_dim/2]");
+    B = t[0]->size(0), H = t[0]->size(1), cap = t[0]->size(2), D = 2 * t[0]->size(3);
+    const int64_t n = D / 16;
+    c.k_codes = static_cast<uint8_t*>(check("k_codes", t[0], at::kByte, {B, H, cap, D / 2}, dev, of));
+    c.k_scales = static_cast<uint8_t*>(check("k_scales", t[1], at::kByte, {B, H, cap, n}, dev, of));
+    c.v_codes = static_cast<uint8_t*>(check("v_codes", t[2], at::kByte, {B, H, cap / 2, D}, dev, of));
+    c.v_scales = static_cast<uint8_t*>(check("v_scales", t[3], at::kByte, {B, H, cap / 2, n, 2}, dev, of));
+    c.batch = int32_of("batch", B);
+    c.heads_kv = int32_of("heads_kv", H);
+    c.head_dim = int32_of("head_dim", D);
+    c.capacity = int32_of("capacity", cap);
+  }
+
+ private:
+  PyObject* hold;
+};
+
+// Angles [n, D/2] or [B, n, D/2], or none.
+const float* rope_arg(const char* name, PyObject* o, int64_t B, int64_t n, int64_t half, int dev, int64_t* stride) {
+  *stride = 0;
+  if (o == Py_None) return nullptr;
+  const at::Tensor* t = tensor(o);
+  if (t != nullptr && t->dim() == 3) {
+    *stride = n * half;
+    return static_cast<const float*>(check(name, t, at::kFloat, {B, n, half}, dev));
+  }
+  return static_cast<const float*>(check(name, t, at::kFloat, {n, half}, dev));
+}
+
+// An output: the caller's, or a new one (owned: returned to Python).
+struct Out {
+  at::Tensor t;
+  void* p = nullptr;
+  Out(const char* name, PyObject* given, at::ScalarType type, at::IntArrayRef shape, int dev) {
+    if (given != Py_None) {
+      p = check(name, tensor(given), type, shape, dev);
+      t = THPVariable_Unpack(given);
+    } else {
+      t = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev));
+      p = t.data_ptr();
+    }
+  }
+};
+
+// The caller's object again (not a new wrapper), or the new tensor's.
+PyObject* result(PyObject* given, const Out& o) { return given != Py_None ? Py_NewRef(given) : THPVariable_Wrap(o.t); }
+
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* r = a != nullptr && b != nullptr ? PyTuple_New(2) : nullptr;
+  if (r == nullptr) {
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(r, 0, a);
+  PyTuple_SET_ITEM(r, 1, b);
+  return r;
+}
+
+// Calls f(stream) on device `dev`, other Python threads running meanwhile.
+template <typename F>
+void run(const char* name, int dev, PyObject* stream, F&& f) {
+  void* handle;
+  if (stream == Py_None) {
+    handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+  } else {
+    PyObject* n = PyObject_GetAttrString(stream, "cuda_stream");
+    if (n == nullptr) throw Refused{};
+    handle = PyLong_AsVoidPtr(n);
+    Py_DECREF(n);
+    if (handle == nullptr && PyErr_Occurred()) throw Refused{};
+  }
+  int st;
+  {
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    PyThreadState* state = PyEval_SaveThread();
+    st = f(handle);
+    PyEval_RestoreThread(state);
+  }
+  if (st != MAGI_BCA_OK) {
+    PyObject* e = PyObject_CallFunction(g_entry.error, "is", st, name);
+    if (e == nullptr) throw Refused{};
+    PyErr_SetObject((PyObject*)Py_TYPE(e), e);
+    Py_DECREF(e);
+    throw Refused{};
+  }
+}
+
+// The caller's workspace or a new one.
+struct Workspace {
+  void* p = nullptr;
+  size_t bytes = 0;
+  at::Tensor made;
+  template <typename F>
+  Workspace(PyObject* given, F size, const magi_bca_kv4_cache& c, const magi_bca_kv4_query& q, int dev) {
+    if (given == Py_None) {
+      bytes = size(&c, &q);
+      if (bytes == 0) return;
+      made = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+      p = made.data_ptr();
+      return;
+    }
+    const at::Tensor* t = tensor(given);
+    if (t == nullptr || !t->is_cuda() || !t->is_contiguous())
+      refuse(PyExc_TypeError, "workspace must be a contiguous CUDA tensor");
+    if (t->get_device() != dev)
+      refuse(PyExc_ValueError,
+             "workspace is on " + t->device().str() + ", the call runs on cuda:" + std::to_string(dev));
+    p = t->data_ptr();
+    bytes = t->nbytes();
+  }
+  // One made here (on the current stream) and used on another stream must not be
+  // handed out again before that stream is done with it.
+  void keep(PyObject* stream) {
+    if (!made.defined() || stream == Py_None ||
+        c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+      return;
+    PyObject* w = THPVariable_Wrap(made);
+    PyObject* r = w != nullptr ? PyObject_CallMethod(w, "record_stream", "O", stream) : nullptr;
+    Py_XDECREF(w);
+    if (r == nullptr) throw Refused{};
+    Py_DECREF(r);
+  }
+};
+
+// What fwd and weights share: the query side and the cache.
+struct QueryArg {
+  int dev;
+  int64_t B, Sq, Hq, D, stride;
+  const uint16_t* q;
+  const float *gamma_q, *gamma_k, *rope;
+  magi_bca_kv4_query query;
+  QueryArg(PyObject* q_, CacheArg& cache, PyObject* gq, PyObject* gk, PyObject* rope_, PyObject* scale, PyObject* eps) {
+    const at::Tensor& t = first("q", q_);
+    dev = t.get_device();
+    cache.look(dev);
+    B = t.size(0), Sq = t.size(1), Hq = t.size(2), D = t.size(3);
+    if (cache.B != B || cache.D != D)
+      refuse(PyExc_ValueError, "q has shape " + text_of(t.sizes()) + ", the cache holds batch " +
+                                   std::to_string(cache.B) + ", heads of " + std::to_string(cache.D));
+    if (Sq < 1) refuse(PyExc_ValueError, "q has no tokens");
+    rope = rope_arg("rope_q", rope_, B, Sq, D / 2, dev, &stride);
+    q = static_cast<const uint16_t*>(check("q", &t, at::kBFloat16, {B, Sq, Hq, D}, dev));
+    gamma_q = check<const float>("gamma_q", gq, at::kFloat, {D}, dev);
+    gamma_k = check<const float>("gamma_k", gk, at::kFloat, {D}, dev);
+    query = magi_bca_kv4_query{int32_of("seqlen_q", Sq), int32_of("heads_q", Hq), float_arg(scale), float_arg(eps), stride};
+  }
+};
+
+// append(k, v, cache, start, counts, rope_k, rms_eps, stream)
+PyObject* append_(PyObject* const* a) {
+  const at::Tensor& k = first("k", a[0]);
+  const int dev = k.get_device();
+  const int64_t B = k.size(0), n = k.size(1), H = k.size(2), D = k.size(3);
+  CacheArg cache(a[2]);
+  cache.look(dev);
+  if (cache.B != B || cache.H != H || cache.D != D)
+    refuse(PyExc_ValueError, "k has shape " + text_of(k.sizes()) + ", the cache holds batch " + std::to_string(cache.B) +
+                                 ", " + std::to_string(cache.H) + " heads of " + std::to_string(cache.D));
+  if (n < 1) return Py_NewRef(Py_None);
+  int64_t stride;
+  const float* rope = rope_arg("rope_k", a[5], B, n, D / 2, dev, &stride);
+  const auto* kp = static_cast<const uint16_t*>(check("k", &k, at::kBFloat16, {B, n, H, D}, dev));
+  const auto* vp = check<const uint16_t>("v", a[1], at::kBFloat16, {B, n, H, D}, dev);
+  const auto* start = check<const int32_t>("start", a[3], at::kInt, {B}, dev);
+  const auto* counts = a[4] == Py_None ? nullptr : check<const int32_t>("counts", a[4], at::kInt, {B}, dev);
+  const int32_t nn = int32_of("n", n);
+  const float eps = float_arg(a[6]);
+  run("magi_bca_kv4_append", dev, a[7],
+      [&](void* s) { return g_entry.append(kp, vp, &cache.c, start, counts, nn, rope, stride, eps, s); });
+  return Py_NewRef(Py_None);
+}
+
+// read(cache, start, n, k, v, stream)
+PyObject* read_(PyObject* const* a) {
+  CacheArg cache(a[0]);
+  const int dev = first("cache.k_codes", cache.t[0]).get_device();
+  cache.look(dev);
+  const int32_t n = int_arg("n", a[2]);
+  if (n < 0) refuse(PyExc_ValueError, "n is negative");
+  const std::array<int64_t, 4> shape = {cache.B, n, cache.H, cache.D};
+  const Out k("k", a[3], at::kBFloat16, shape, dev), v("v", a[4], at::kBFloat16, shape, dev);
+  const auto* start = a[1] == Py_None ? nullptr : check<const int32_t>("start", a[1], at::kInt, {cache.B}, dev);
+  if (n > 0)
+    run("magi_bca_kv4_read", dev, a[5], [&](void* s) {
+      return g_entry.read(&cache.c, start, n, static_cast<uint16_t*>(k.p), static_cast<uint16_t*>(v.p), s);
+    });
+  return pair(result(a[3], k), result(a[4], v));
+}
+
+// fwd(q, cache, lengths, gamma_q, gamma_k, rope_q, base_out, base_lse, out, lse, softmax_scale, rms_eps, want_lse,
+//     workspace, stream)
+PyObject* fwd_(PyObject* const* a) {
+  CacheArg cache(a[1]);
+  const QueryArg q(a[0], cache, a[3], a[4], a[5], a[10], a[11]);
+  const std::array<int64_t, 4> shape = {q.B, q.Sq, q.Hq, q.D};
+  const std::array<int64_t, 3> rows = {q.B, q.Hq, q.Sq};
+  if ((a[6] == Py_None) != (a[7] == Py_None)) refuse(PyExc_ValueError, "base_out and base_lse go together");
+  const bool base = a[6] != Py_None;
+  const auto* base_out = base ? check<const uint16_t>("base_out", a[6], at::kBFloat16, shape, q.dev) : nullptr;
+  const auto* base_lse = base ? check<const float>("base_lse", a[7], at::kFloat, rows, q.dev) : nullptr;
+  const auto* lengths = check<const int32_t>("lengths", a[2], at::kInt, {q.B}, q.dev);
+  const int want = a[9] != Py_None ? 1 : PyObject_IsTrue(a[12]);
+  if (want < 0) throw Refused{};
+  const Out out("out", a[8], at::kBFloat16, shape, q.dev);
+  std::optional<Out> lse;
+  if (want) lse.emplace("lse", a[9], at::kFloat, rows, q.dev);
+  Workspace w(a[13], g_entry.fwd_size, cache.c, q.query, q.dev);
+  run("magi_bca_kv4_fwd", q.dev, a[14], [&](void* s) {
+    return g_entry.fwd(q.q, &cache.c, lengths, q.gamma_q, q.gamma_k, q.rope, base_out, base_lse,
+                       static_cast<uint16_t*>(out.p), lse ? static_cast<float*>(lse->p) : nullptr, w.p, w.bytes, &q.query, s);
+  });
+  w.keep(a[14]);
+  return pair(result(a[8], out), lse ? result(a[9], *lse) : Py_NewRef(Py_None));
+}
+
+// weights(q, cache, lengths, lse, gamma_q, gamma_k, weights, rope_q, decay, softmax_scale, rms_eps, workspace, stream)
+PyObject* weights_(PyObject* const* a) {
+  CacheArg cache(a[1]);
+  const QueryArg q(a[0], cache, a[4], a[5], a[7], a[9], a[10]);
+  const auto* lse = check<const float>("lse", a[3], at::kFloat, {q.B, q.Hq, q.Sq}, q.dev);
+  auto* weights = check<float>("weights", a[6], at::kFloat, {q.B, cache.H, cache.cap}, q.dev);
+  const auto* lengths = check<const int32_t>("lengths", a[2], at::kInt, {q.B}, q.dev);
+  const float decay = float_arg(a[8]);
+  Workspace w(a[11], g_entry.weights_size, cache.c, q.query, q.dev);
+  run("magi_bca_kv4_weights", q.dev, a[12], [&](void* s) {
+    return g_entry.weights(q.q, &cache.c, lengths, lse, q.gamma_q, q.gamma_k, q.rope, weights, decay, w.p, w.bytes, &q.query, s);
+  });
+  w.keep(a[12]);
+  return Py_NewRef(a[6]);
+}
+
+// evict(cache, weights, lengths, keep, recent, dst_cache, dst_weights, dst_lengths, index, stream)
+PyObject* evict_(PyObject* const* a) {
+  CacheArg cache(a[0]), dst(a[5]);
+  const int dev = first("cache.k_codes", cache.t[0]).get_device();
+  cache.look(dev);
+  dst.look(dev, "dst_cache.");
+  if (dst.B != cache.B || dst.H != cache.H || dst.D != cache.D)
+    refuse(PyExc_ValueError, "dst_cache must have the cache's batch, heads and head_dim");
+  const int32_t keep = int_arg("keep", a[3]), recent = int_arg("recent", a[4]);
+  if (!(1 <= keep && keep <= dst.cap && 0 <= recent && recent <= keep))
+    refuse(PyExc_ValueError, "need 1 <= keep <= " + std::to_string(dst.cap) + " and 0 <= recent <= keep (got " +
+                                 std::to_string(keep) + ", " + std::to_string(recent) + ")");
+  const auto* w = check<const float>("weights", a[1], at::kFloat, {cache.B, cache.H, cache.cap}, dev);
+  auto* dw = check<float>("dst_weights", a[6], at::kFloat, {cache.B, cache.H, dst.cap}, dev);
+  const auto* lengths = check<const int32_t>("lengths", a[2], at::kInt, {cache.B}, dev);
+  const Out left("dst_lengths", a[7], at::kInt, {cache.B}, dev), index("index", a[8], at::kInt, {cache.B, cache.H, keep}, dev);
+  run("magi_bca_kv4_evict", dev, a[9], [&](void* s) {
+    return g_entry.evict(&cache.c, w, lengths, keep, recent, &dst.c, dw, static_cast<int32_t*>(left.p),
+                         static_cast<int32_t*>(index.p), s);
+  });
+  return pair(result(a[7], left), result(a[8], index));
+}
+
+template <PyObject* (*F)(PyObject* const*), int N>
+PyObject* method(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%d arguments expected, not %zd", N, n);
+    return nullptr;
+  }
+  if (g_entry.error == nullptr) {
+    PyErr_SetString(PyExc_RuntimeError, "bind() was not called");
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Refused&) {
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
+  }
+  return nullptr;
+}
+
+// bind(error, append, read, fwd, weights, evict, fwd_workspace_size, weights_workspace_size): addresses as integers
+PyObject* bind(PyObject*, PyObject* args) {
+  PyObject* error;
+  unsigned long long f[7];
+  if (!PyArg_ParseTuple(args, "OKKKKKKK", &error, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6)) return nullptr;
+  PyObject* was = g_entry.error;
+  g_entry = Entry{reinterpret_cast<decltype(g_entry.append)>(f[0]), reinterpret_cast<decltype(g_entry.read)>(f[1]),
+                  reinterpret_cast<decltype(g_entry.fwd)>(f[2]), reinterpret_cast<decltype(g_entry.weights)>(f[3]),
+                  reinterpret_cast<decltype(g_entry.evict)>(f[4]), reinterpret_cast<decltype(g_entry.fwd_size)>(f[5]),
+                  reinterpret_cast<decltype(g_entry.weights_size)>(f[6]), Py_NewRef(error)};
+  Py_XDECREF(was);
+  Py_RETURN_NONE;
+}
+
+template <PyObject* (*F)(PyObject* const*), int N>
+PyMethodDef fast(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&method<F, N>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef g_methods[] = {{"bind", bind, METH_VARARGS, nullptr},
+                           fast<append_, 8>("append"),
+                           fast<read_, 6>("read"),
+                           fast<fwd_, 15>("fwd"),
+                           fast<weights_, 13>("weights"),
+                           fast<evict_, 10>("evict"),
+                           {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_kv4_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__kv4_binding() { return PyModule_Create(&g_module); }

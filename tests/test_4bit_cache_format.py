@@ -207,3 +207,18 @@ def test_the_binding_refuses_cpu_tensors_and_bad_shapes():
         bca.magi_bca_kv4_cache(1, 2, 80, 128, device="cpu")
     with pytest.raises(ValueError):
         bca.magi_bca_kv4_cache(0, 2, 64, 128, device="cpu")
+
+
+def test_the_binding_refuses_what_is_no_cache():
+    c = bca.magi_bca_kv4_cache(1, 2, 64, 128, device="cpu")
+    q, n, one = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.ones(64)
+    for bad in (c[:3], (*c, c[0]), ()):
+        with pytest.raises(ValueError, match="four tensors"):
+            bca.magi_bca_kv4_fwd(q, bad, n, one, one)
+        with pytest.raises(ValueError, match="four tensors"):
+            bca.magi_bca_kv4_evict(c, torch.zeros(1, 2, 128), n, 4, 0, bad, torch.zeros(1, 2, 128))
+    for bad in (None, 3, [1, 2, 3, 4]):
+        with pytest.raises(TypeError):
+            bca.magi_bca_kv4_read(bad, n, 3)
+    with pytest.raises(TypeError, match="q must be a CUDA tensor"):
+        bca.magi_bca_kv4_fwd(None, c, n, one, one)

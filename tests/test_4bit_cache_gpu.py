@@ -507,3 +507,65 @@ def test_binding_refusals():
         with pytest.raises(bca.MagiBcaError) as e:
             bad()
         assert e.value.status == status
+
+
+def test_binding_refusals_say_what_was_expected():
+    c = bca.magi_bca_kv4_cache(2, 2, 64, 128)
+    k = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    n, one = ints(1, 1), torch.ones(64, device=DEV)
+    w = torch.zeros(2, 2, 128, device=DEV)
+    to = bca.magi_bca_kv4_cache(2, 2, 64, 128)
+    q = torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    for bad, kind, text in (
+            (lambda: bca.magi_bca_kv4_append(c, k, k, ints(1)), ValueError, r"start has shape \(1,\), expected \(2,\)"),
+            (lambda: bca.magi_bca_kv4_append(c, k, k.float(), n), TypeError, "v must be a contiguous bfloat16 CUDA tensor"),
+            (lambda: bca.magi_bca_kv4_append(c, k[0], k[0], n), ValueError, r"k has shape \(3, 2, 64\), expected 4 dimensions"),
+            (lambda: bca.magi_bca_kv4_append(c, k, k, n, rms_eps="x"), TypeError, "real number"),
+            (lambda: bca.magi_bca_kv4_read(c, n, -1), ValueError, "n is negative"),
+            (lambda: bca.magi_bca_kv4_read(c, n, 1 << 40), ValueError, "n is out of range"),
+            (lambda: bca.magi_bca_kv4_read(c, n, 3, k=k[:, :2].contiguous()), ValueError, r"k has shape \(2, 2, 2, 64\)"),
+            (lambda: bca.magi_bca_kv4_fwd(q, (c[0], c[1][..., :2].contiguous(), *c[2:]), n, one, one), ValueError,
+             r"cache.k_scales has shape \(2, 2, 128, 2\), expected \(2, 2, 128, 4\)"),
+            (lambda: bca.magi_bca_kv4_fwd(q, c, n, one, one, workspace=torch.zeros(8)), TypeError, "workspace must be"),
+            (lambda: bca.magi_bca_kv4_fwd(q, c, n, one, one, stream=5), AttributeError, "cuda_stream"),
+            (lambda: bca.magi_bca_kv4_evict(c, w, n, 5, 6, to, w.clone()), ValueError, r"0 <= recent <= keep \(got 5, 6\)"),
+            (lambda: bca.magi_bca_kv4_evict(c, w, n, 1 << 70, 0, to, w.clone()), ValueError, "keep is out of range")):
+        with pytest.raises(kind, match=text):
+            bad()
+    # what was refused left the calls usable, and given outputs come back as themselves
+    out, lse = torch.empty_like(q), torch.empty(2, 4, 1, device=DEV)
+    got = bca.magi_bca_kv4_fwd(q, c, n, one, one, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    assert bca.magi_bca_kv4_fwd(q, c, n, one, one, want_lse=False)[1] is None
+    assert bca.magi_bca_kv4_weights(q, c, n, lse, one, one, w) is w
+    assert all(x.shape == (2, 0, 2, 64) for x in bca.magi_bca_kv4_read(c, n, 0))
+    assert bca.magi_bca_last_device_status() == 0
+
+
+def test_calls_from_several_threads():
+    """Each thread on its own stream; the answers are those of one thread."""
+    import threading
+    g = gen(37)
+    D, cap = 64, 2048
+    cache = filled(g, 1, 2, D, cap, [2000])
+    q = randn(g, 1, 2, 4, D).bfloat16()
+    gq, gk = gains(g, D)
+    n = ints(2000)
+    want = bca.magi_bca_kv4_fwd(q, cache, n, gq, gk)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                got = bca.magi_bca_kv4_fwd(q, cache, n, gq, gk)
+                s.synchronize()
+                if not (torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])):
+                    wrong.append(1)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
