@@ -53,7 +53,7 @@ def build_binding(force=False):
     # wrappers link in) does not go with torch's
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + i for i in include),
            "-o", BINDING, os.path.join(CSRC, "kv4_binding.cpp"), "-L" + os.path.join(torch, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10_cuda", "-lc10"]
     subprocess.run(cmd, check=True)
     return BINDING
 

@@ -5,14 +5,18 @@
 // NaN counts as -inf).  Order is kept.
 //
 // Selection (kv4_select_kernel).  A weight is mapped to an unsigned integer of
-// the same order and the need-th largest is found digit by digit (11, 11 and
-// 10 bits), a histogram of the candidates with the digits so far at each.  A
+// the same order and the need-th largest is found digit by digit (12, 12 and 8
+// bits), a histogram of the candidates with the digits so far at each.  A
 // cluster of 8 CTAs shares a head: each keeps the keys of an eighth in shared
-// memory, counts them there and adds its counts that are not zero to the
-// totals of all eight through distributed shared memory (a few hundred bins;
-// reading all eight histograms whole took five times as long).  The kept
-// tokens are then numbered in their order by ballots: a warp takes a
-// contiguous run and starts at the counts of the runs before it.
+// memory and counts them there, by bin and by group of 64 bins.  One warp of
+// each CTA then reads the eight CTAs' group counts through distributed shared
+// memory, finds the group that holds the need-th, and in its 64 bins the bin.
+// (Adding every count that is not zero to totals of all eight CTAs took up to
+// 8300 cycles a digit: 66.7 us for 16 heads of 92160 against 60.3 in all, 10.8
+// against 11.2 for 8 heads of 4097; sending the group counts instead of having
+// them read 61.5 and 11.8.)
+// The kept tokens are then numbered in their order: a warp takes a contiguous
+// run and starts at the counts of the runs before it.
 //
 // Moving (kv4_move_kernel).  Bound by bytes: a kept token is read and written
 // once.  A row of the value cache holds two tokens, so a destination row is
@@ -31,7 +35,9 @@ namespace {
 
 constexpr int kCluster = 8;
 constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
+constexpr int kBins = 4096;         // of the first two digits
+constexpr int kLastBins = 256;
+constexpr int kGroup = 64, kGroups = kBins / kGroup;   // bins are counted by group too; two of each a lane
 
 // Order-preserving integer of a weight.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -44,13 +50,38 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 40 * 1024;   // keys a CTA keeps; longer runs are read again each time
 
 struct SelShared {
-  uint32_t hist[kBins];      // this CTA's counts
-  uint32_t total[3][kBins];  // the cluster's
-  uint32_t scan[kSelWarps];
+  uint32_t hist[2 * kBins + kLastBins];   // this CTA's counts, each digit its own
+  uint32_t group[3][kGroups];
   uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
   uint32_t cta_gt, cta_eq;
-  uint32_t bin, above;
+  uint32_t bin, left;
 };
+static_assert(sizeof(SelShared) % 16 == 0, "the keys behind it are read 16 bytes at a time");
+
+// Of 64 counts (two a lane, `at` summed over the cluster's CTAs) the one, from
+// the top, in which the left-th lies; left becomes its place in there.
+__device__ __forceinline__ uint32_t pick(cg::cluster_group& cluster, uint32_t* at, uint32_t& left) {
+  const int lane = threadIdx.x & 31;
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) {
+    const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(at, r) + 62 - 2 * lane);
+    lo += v.x;
+    hi += v.y;
+  }
+  uint32_t incl = lo + hi;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  const uint32_t before = incl - lo - hi;
+  const int at_lane = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;   // (the counts' sum is at least left)
+  const bool in_hi = before + hi >= left;
+  const uint32_t bin = in_hi ? 63 - 2 * lane : 62 - 2 * lane, place = left - before - (in_hi ? 0u : hi);
+  left = __shfl_sync(0xffffffffu, place, at_lane);
+  return __shfl_sync(0xffffffffu, bin, at_lane);
+}
 
 // Candidates of a CTA, and of one of its warps (a multiple of 128: a lane takes
 // four neighbours at a time).
@@ -64,6 +95,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.y, b = bh / p.src.heads;
+  for (int i = tid; i < (int)(sizeof(sh.hist) / 16); i += kSelThreads)
+    reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 3 * kGroups) (&sh.group[0][0])[tid] = 0;
+  __syncthreads();
   let_next_start();
   wait_for_previous();
   const int len = min(max(p.lengths[b], 0), p.src.cap);
@@ -86,71 +121,77 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
     return make_uint4(order_key(x.x), o + 1 < len_w ? order_key(x.y) : 0u, o + 2 < len_w ? order_key(x.z) : 0u,
                       o + 3 < len_w ? order_key(x.w) : 0u);
   };
-  if (held) {
-#pragma unroll 4
-    for (int o = lane * 4; o < len_w; o += 128) *reinterpret_cast<uint4*>(keys + o) = from_row(o);
-  }
   auto four = [&](int o) {
     if (o >= len_w) return make_uint4(0, 0, 0, 0);
     return held ? *reinterpret_cast<const uint4*>(keys + o) : from_row(o);
   };
+  const bool search = need > 0 && need < n;      // the same for the whole cluster
+  auto count = [&](uint32_t key, int shift, uint32_t mask, uint32_t* hist) {
+    if (key != 0) atomicAdd(hist + ((key >> shift) & mask), 1u);
+  };
+
+  // keys into shared memory and the first digit's counts, four loads under way a lane
+  if (held || search)
+    for (int o0 = lane * 4; o0 < len_w; o0 += 512) {
+      uint4 k[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        k[j] = o0 + 128 * j < len_w ? from_row(o0 + 128 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (o0 + 128 * j >= len_w) continue;
+        if (held) *reinterpret_cast<uint4*>(keys + o0 + 128 * j) = k[j];
+        if (search) {
+          count(k[j].x, 20, kBins - 1, sh.hist);
+          count(k[j].y, 20, kBins - 1, sh.hist);
+          count(k[j].z, 20, kBins - 1, sh.hist);
+          count(k[j].w, 20, kBins - 1, sh.hist);
+        }
+      }
+    }
 
   // the need-th largest key and how many of those equal to it stay
   uint32_t top = need == 0 ? 0xffffffffu : 0u;   // all stay: every key is above
   uint32_t ties = 0;
-  if (need > 0 && need < n) {                    // the same for the whole cluster
+  if (search) {
     uint32_t prefix = 0, left = (uint32_t)need;
-    for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = sh.total[0][i] = sh.total[1][i] = sh.total[2][i] = 0;
-    cluster.sync();
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bits = pass == 2 ? 10 : 11;
-      auto count = [&](uint32_t key) {
-        if (key != 0 && (pass == 0 || (key >> (shift + bits)) == prefix))
-          atomicAdd(&sh.hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
-      };
-      for (int o = lane * 4; o < len_w; o += 128) {
-        const uint4 k = four(o);
-        count(k.x);
-        count(k.y);
-        count(k.z);
-        count(k.w);
+      const int shift = pass == 0 ? 20 : pass == 1 ? 8 : 0;
+      const int bits = pass == 2 ? 8 : 12;
+      uint32_t* hist = sh.hist + pass * kBins;
+      if (pass > 0) {
+        auto of_prefix = [&](uint32_t key) {
+          if ((key >> (shift + bits)) == prefix) count(key, shift, (1u << bits) - 1u, hist);
+        };
+        for (int o = lane * 4; o < len_w; o += 128) {
+          const uint4 k = four(o);
+          of_prefix(k.x);
+          of_prefix(k.y);
+          of_prefix(k.z);
+          of_prefix(k.w);
+        }
       }
       __syncthreads();
-      for (int i = tid; i < kBins; i += kSelThreads) {
-        const uint32_t v = sh.hist[i];
-        if (v == 0) continue;
-        sh.hist[i] = 0;
+      if (tid < (1 << bits) / 4) {   // whole warps; 16 lanes a group
+        const uint4 v = reinterpret_cast<const uint4*>(hist)[tid];
+        uint32_t sum = v.x + v.y + v.z + v.w;
 #pragma unroll
-        for (int r = 0; r < kCluster; ++r) atomicAdd(cluster.map_shared_rank(&sh.total[pass][i], r), v);
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane % 16 == 0) sh.group[pass][tid / 16] = sum;
       }
       cluster.sync();
-      // thread t holds the counts of its bins from the top
-      constexpr int kPer = kBins / kSelThreads;
-      uint32_t cnt[kPer], mine = 0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) mine += cnt[k] = sh.total[pass][kBins - 1 - (tid * kPer + k)];
-      uint32_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[lane] : 0u);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (before < left && before + cnt[k] >= left) {   // exactly one bin
-          sh.bin = (uint32_t)(kBins - 1 - (tid * kPer + k));
-          sh.above = before;
+      if (warp == 0) {
+        const uint32_t g = pick(cluster, sh.group[pass], left);
+        const uint32_t in_group = pick(cluster, hist + g * kGroup, left);
+        if (lane == 0) {
+          sh.bin = g * kGroup + in_group;
+          sh.left = left;
         }
-        before += cnt[k];
       }
       __syncthreads();
       prefix = (prefix << bits) | sh.bin;
-      left -= sh.above;
+      left = sh.left;
     }
     top = prefix;
     ties = left;
@@ -184,20 +225,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads) 
   gt0 = __reduce_add_sync(0xffffffffu, gt0 + (lane < warp ? sh.warp_gt[lane] : 0u));
   eq0 = __reduce_add_sync(0xffffffffu, eq0 + (lane < warp ? sh.warp_eq[lane] : 0u));
   cluster.sync();   // no CTA leaves while its shared memory is read
-  const uint32_t below = (1u << lane) - 1u;
   for (int o0 = 0; o0 < len_w; o0 += 128) {
     const int o = o0 + lane * 4;
     const uint4 k4 = four(o);
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    uint32_t g = gt0, e = eq0;   // before this lane's first
+    uint32_t mine = 0;   // above the threshold, and equal to it in the upper half
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t mg = __ballot_sync(0xffffffffu, k[c] > top), me = __ballot_sync(0xffffffffu, k[c] == top);
-      g += __popc(mg & below);
-      e += __popc(me & below);
-      gt0 += __popc(mg);
-      eq0 += __popc(me);
+    for (int c = 0; c < 4; ++c) mine += (k[c] > top ? 1u : 0u) + (k[c] == top ? 0x10000u : 0u);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += x;
     }
+    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+    uint32_t g = gt0 + ((incl - mine) & 0xffffu), e = eq0 + ((incl - mine) >> 16);   // before this lane's first
+    gt0 += all & 0xffffu;
+    eq0 += all >> 16;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (k[c] > top) {

@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -154,6 +155,10 @@ const float* rope_arg(const char* name, PyObject* o, int64_t B, int64_t n, int64
   return static_cast<const float*>(check(name, t, at::kFloat, {n, half}, dev));
 }
 
+at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
+}
+
 // An output: the caller's, or a new one (owned: returned to Python).
 struct Out {
   at::Tensor t;
@@ -163,7 +168,7 @@ struct Out {
       p = check(name, tensor(given), type, shape, dev);
       t = THPVariable_Unpack(given);
     } else {
-      t = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev));
+      t = make(shape, type, dev);
       p = t.data_ptr();
     }
   }
@@ -223,7 +228,7 @@ struct Workspace {
     if (given == Py_None) {
       bytes = size(&c, &q);
       if (bytes == 0) return;
-      made = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+      made = make({(int64_t)bytes}, at::kByte, dev);
       p = made.data_ptr();
       return;
     }
