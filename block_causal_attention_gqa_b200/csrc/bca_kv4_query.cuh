@@ -30,26 +30,28 @@ __device__ __forceinline__ void fold_query(const FwdParams4& p, int b, int hk, i
   if (row < rows) {   // warp-uniform
     const int h = hk * G + row / p.sq, i = row % p.sq;
     const uint16_t* src = p.q + (((int64_t)b * p.sq + i) * p.heads_q + h) * D + lane * E;
-    if constexpr (E == 4) {
-      const uint2 w = *(reinterpret_cast<const uint2*>(src));
-      x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-    } else {
-      const uint32_t w = *(reinterpret_cast<const uint32_t*>(src));
-      x[0] = bf16_lo(w); x[1] = bf16_hi(w);
-    }
-    float gain[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) gain[e] = query_gain(p, lane * E + e);
-    const float r = rms_inv<D>(warp_sumsq_row<E>(x), p.eps);
+    // all loads first: the prologue is as long as the memory is far
+    float a[E] = {}, gain[E];
     if (p.rope != nullptr) {
-      // the pair of feature d is d +- D/2, half the warp away
       const float* ang = p.rope + (int64_t)b * p.rope_stride + (int64_t)i * (D / 2) + (lane & 15) * E;
-      float a[E], sn[E], cs[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) a[e] = ang[e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) gain[e] = query_gain(p, lane * E + e);
+    if constexpr (E == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(src);
+      x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+    } else {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(src);
+      x[0] = bf16_lo(w); x[1] = bf16_hi(w);
+    }
+    const float r = rms_inv<D>(warp_sumsq_row<E>(x), p.eps);
+    if (p.rope != nullptr) {
+      float sn[E], cs[E];
       sincos_row<E>(a, sn, cs);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < E; ++e) {   // the pair of feature d is d +- D/2, half the warp away
         const float o = __shfl_xor_sync(0xffffffffu, x[e], 16);
         x[e] = lane < 16 ? rope_first(x[e], o, cs[e], sn[e]) : rope_second(o, x[e], cs[e], sn[e]);
       }
