@@ -69,8 +69,8 @@ constexpr float kLift = 7.f;           // P carries a factor 2^kLift
 
 enum : int { kErrRing = 3101, kErrRingW = 3102 };
 
-// NT: row groups of 4 a CTA takes.
-template <int D, int NT>
+// NT: row groups of 4 a CTA takes; W: its warps.
+template <int D, int NT, int W>
 struct Ring {
   static constexpr int kRows = 4 * NT;
   static constexpr int kKc = kStep * D / 2, kKs = kStep * D / 16, kVc = kKc, kVs = kKs;   // a stage: kc, vc, ks, vs
@@ -78,10 +78,10 @@ struct Ring {
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kQ = NT * (D / 16) * 32 * 8;       // query fragments of a row tile
   static constexpr int kMergeRow = D + 4;                 // floats, padded
-  static constexpr int kMerge = kWarps * kRows * kMergeRow * 4;
-  static constexpr int kRing = kWarps * kWarp;
+  static constexpr int kMerge = W * kRows * kMergeRow * 4;
+  static constexpr int kRing = W * kWarp;
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;   // the merge reuses the ring
-  static constexpr int kTotal = kBody + kQ + (kWarps + 1) * kRows * 8 + kWarps * kStages * 8;
+  static constexpr int kTotal = kBody + kQ + (W + 1) * kRows * 8 + W * kStages * 8;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
@@ -211,15 +211,15 @@ __device__ __forceinline__ int4 find_part(const FwdParams4& p, int per, int lane
 }
 
 // kCluster: one history per cluster, one piece per CTA.
-template <int D, int NT, bool kCluster>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kernel(const FwdParams4 p) {
-  using R = Ring<D, NT>;
+template <int D, int NT, int W, bool kCluster>
+__global__ void __launch_bounds__(W * 32, W == kWarps ? (NT == 1 ? 4 : 3) : 1) kv4_token_fwd_kernel(const FwdParams4 p) {
+  using R = Ring<D, NT, W>;
   constexpr int kRows = R::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   float* smem_merge = reinterpret_cast<float*>(smem);
   uint8_t* smem_q = smem + R::kBody;
   float2* smem_ml = reinterpret_cast<float2*>(smem_q + R::kQ);            // [warp][row], then the CTA's [row]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_ml + (kWarps + 1) * kRows);   // [warp][stage]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_ml + (W + 1) * kRows);   // [warp][stage]
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int G = p.heads_q / p.c.heads, rows = G * p.sq;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     const int64_t slot = (int64_t)blockIdx.x + (int64_t)b * per + hist;   // of the workspace
     x += s_end - s_begin;
 
-    const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + kWarps - 1) / kWarps : 0;
+    const int n_steps = s_end - s_begin > warp ? (s_end - s_begin - warp + W - 1) / W : 0;
     const int64_t at0 = (int64_t)bh * p.c.cap + (int64_t)(s_begin + warp) * kStep;
     const uint8_t *src_kc = p.c.kc + at0 * (D / 2), *src_vc = p.c.vc + at0 / 2 * D;
     const uint8_t *src_ks = p.c.ks + at0 * (D / 16), *src_vs = p.c.vs + at0 * (D / 16);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
       if (elect_one()) {
         const uint32_t st = (it + k) % kStages;
         uint8_t* dst = ring + st * R::kStage;
-        const int64_t codes = (int64_t)k * (kWarps * R::kKc), scales = (int64_t)k * (kWarps * R::kKs);
+        const int64_t codes = (int64_t)k * (W * R::kKc), scales = (int64_t)k * (W * R::kKs);
         mbar_arrive_expect_tx(bar + st, R::kStage);
         bulk_load(dst, src_kc + codes, R::kKc, bar + st);
         bulk_load(dst + R::kKc, src_vc + codes, R::kVc, bar + st);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     for (int k = 0; k < min(n_steps, kStages); ++k) issue(k);
 
     // the row tile's queries, while the first copies are under way
-    for (int i = warp; i < kRows; i += kWarps)
+    for (int i = warp; i < kRows; i += W)
       fold_query_fragment<D>(p, b, hk, G, row0 + i, rows, i & 3, lane, smem_q + (i >> 2) * (D / 16) * 32 * 8);
     __syncthreads();
     uint32_t q[NT][D / 16][2];
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
       const uint8_t* vc = kc + R::kKc;
       const uint8_t* ks = vc + R::kVc;
       const uint8_t* vs = ks + R::kKs;
-      const int tok = (s_begin + warp + k * kWarps) * kStep;
+      const int tok = (s_begin + warp + k * W) * kStep;
       const bool tail = tok + kStep > len;
       float s[2][4];             // [16 tokens][token g: row r0, r0 + 1; token g + 8: the same]
 #pragma unroll
@@ -443,16 +443,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
     }
     __syncthreads();
 
-    constexpr int kPerRow = kThreads / kRows;            // threads a row
-    constexpr int F = D / kPerRow;                       // features a thread: 4 or 8 (2 at head_dim 64 of 4 rows)
+    constexpr int kPerRow = (W * 32) / kRows;            // threads a row
+    constexpr int F = D / kPerRow;                       // features a thread
     const int i = threadIdx.x / kPerRow, f0 = threadIdx.x % kPerRow * F;
     float mm = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, smem_ml[w * kRows + i].x);
+    for (int w = 0; w < W; ++w) mm = fmaxf(mm, smem_ml[w * kRows + i].x);
     float acc[F] = {}, ll = 0.f;
     if (mm != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float2 ml = smem_ml[w * kRows + i];
         const float sc = fast_exp2(ml.x - mm);
         ll += ml.y * sc;
@@ -465,17 +465,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_token_fwd_kerne
       // the CTA's part in the place of warp 0's (no other thread reads these features), then the cluster's
 #pragma unroll
       for (int f = 0; f < F; ++f) smem_merge[i * R::kMergeRow + f0 + f] = acc[f];
-      if (f0 == 0) smem_ml[kWarps * kRows + i] = make_float2(mm, ll);
+      if (f0 == 0) smem_ml[W * kRows + i] = make_float2(mm, ll);
       cg::cluster_group cluster = cg::this_cluster();
       cluster.sync();
-      constexpr int kT = D / 2, kAtOnce = kThreads / kT;   // threads a row, two features each
+      constexpr int kT = D / 2, kAtOnce = (W * 32) / kT;   // threads a row, two features each
       for (int r = rank * kAtOnce + threadIdx.x / kT; r < kRows; r += size * kAtOnce) {
         const int f = threadIdx.x % kT * 2;
         float m1 = -INFINITY, l1 = 0.f, o1[2] = {0.f, 0.f};
-        for (int k = 0; k < size; ++k) m1 = fmaxf(m1, cluster.map_shared_rank(smem_ml, k)[kWarps * kRows + r].x);
+        for (int k = 0; k < size; ++k) m1 = fmaxf(m1, cluster.map_shared_rank(smem_ml, k)[W * kRows + r].x);
         if (m1 != -INFINITY)
           for (int k = 0; k < size; ++k) {
-            const float2 ml = cluster.map_shared_rank(smem_ml, k)[kWarps * kRows + r];
+            const float2 ml = cluster.map_shared_rank(smem_ml, k)[W * kRows + r];
             const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(smem_merge, k) + r * R::kMergeRow + f);
             const float w = fast_exp2(ml.x - m1);
             l1 = fmaf(ml.y, w, l1);
@@ -758,6 +758,12 @@ int token_cluster(const Cache& c, int rows) {
   return steps <= 8 * kWarps * size ? size : 0;
 }
 
+// Where a cluster of 16 has more than a step for each warp, its CTAs, which have
+// an SM each, get twice the warps.
+bool token_cluster_is_wide(const Cache& c, int cluster) {
+  return cluster == 16 && (c.cap + kStep - 1) / kStep > kWarps * 16;
+}
+
 // Rows of pieces: (slots) x (rows of a tile); none for clusters.
 int64_t token_piece_rows(const Cache& c, int rows) {
   if (token_cluster(c, rows) > 0) return 0;
@@ -769,23 +775,29 @@ bool token_steps_fit(const Cache& c, int rows) {
   return histories(c, rows, false) * ((c.cap + kStep - 1) / kStep) < (int64_t(1) << 30);
 }
 
+template <int D, int NT, int W>
+static cudaError_t token_fwd_cluster(const FwdParams4& p, int cluster, cudaStream_t s) {
+  using R = Ring<D, NT, W>;
+  static SmemRecord have;
+  const cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, W, true>, R::kTotal, have, true);
+  if (e != cudaSuccess) return e;
+  const int64_t hist = histories(p.c, p.heads_q / p.c.heads * p.sq, false);
+  return launch_early(kv4_token_fwd_kernel<D, NT, W, true>, dim3((unsigned)(hist * cluster)), W * 32, R::kTotal, s, cluster, p);
+}
+
 template <int D, int NT>
 static cudaError_t token_fwd_d(const FwdParams4& p, cudaStream_t s) {
-  using R = Ring<D, NT>;
   const int rows = p.heads_q / p.c.heads * p.sq;
   const int cluster = token_cluster(p.c, rows);
-  if (cluster > 0) {
-    static SmemRecord have;
-    const cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, true>, R::kTotal, have, true);
-    if (e != cudaSuccess) return e;
-    return launch_early(kv4_token_fwd_kernel<D, NT, true>, dim3((unsigned)(histories(p.c, rows, false) * cluster)), kThreads,
-                        R::kTotal, s, cluster, p);
-  }
+  if (cluster > 0)
+    return token_cluster_is_wide(p.c, cluster) ? token_fwd_cluster<D, NT, 2 * kWarps>(p, cluster, s)
+                                               : token_fwd_cluster<D, NT, kWarps>(p, cluster, s);
+  using R = Ring<D, NT, kWarps>;
   static SmemRecord have;
-  cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, false>, R::kTotal, have);
+  cudaError_t e = allow_smem(kv4_token_fwd_kernel<D, NT, kWarps, false>, R::kTotal, have);
   if (e != cudaSuccess) return e;
   const int ctas = token_ctas(p.c, rows, false);
-  kv4_token_fwd_kernel<D, NT, false><<<ctas, kThreads, R::kTotal, s>>>(p);
+  kv4_token_fwd_kernel<D, NT, kWarps, false><<<ctas, kThreads, R::kTotal, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_early(kv4_token_combine_kernel<D>, dim3((unsigned)((int64_t)p.c.batch * p.heads_q * p.sq)), 256, 0, s, 0, p,
