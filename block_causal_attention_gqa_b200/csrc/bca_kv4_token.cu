@@ -44,7 +44,7 @@
 // Short histories (token_cluster() says which) are a matter of latency: there a
 // cluster of up to 16 CTAs takes a history, joins its parts through
 // distributed shared memory and writes the result, in one launch and without a
-// workspace (4096 tokens of 4 heads: 5.1 + 3.9 us in two launches).
+// workspace (4096 tokens of 4 heads: 6.6 us a call, 9.8 as two launches).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -212,7 +212,7 @@ __device__ __forceinline__ int4 find_part(const FwdParams4& p, int per, int lane
 
 // kCluster: one history per cluster, one piece per CTA.
 template <int D, int NT, int W, bool kCluster>
-__global__ void __launch_bounds__(W * 32, W == kWarps ? (NT == 1 ? 4 : 3) : 1) kv4_token_fwd_kernel(const FwdParams4 p) {
+__global__ void __launch_bounds__(W * 32, W == kWarps ? (NT == 1 ? 4 : 3) : 2) kv4_token_fwd_kernel(const FwdParams4 p) {
   using R = Ring<D, NT, W>;
   constexpr int kRows = R::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -748,20 +748,24 @@ int token_ctas(const Cache& c, int rows, bool weights) {
 // end instead.  As many (a power of two) as let all clusters run at once (16 only
 // with a CTA an SM: with more, clusters of 16 wait for one another; 24 of them
 // took 15.5 us where 32 of 8 took 9.2), and no more than have a step for each
-// warp.  Histories of more than 8 steps a warp are left to the balanced split,
-// which then costs less than the uneven ends of clusters.
+// warp.  Longer histories are left to the balanced split, which then costs less
+// than the uneven ends of clusters: those of more than 8 steps a warp, or, with
+// the twice as many warps of an SM for each CTA, 6 (us as split / as clusters;
+// head_dim 128: 8 heads of 24576 tokens 18.2 / 16.2, of 32768 18.5 / 19.5; 16
+// heads of 8192 16.4 / 12.3, of 16384 18.5 / 18.8).
 int token_cluster(const Cache& c, int rows) {
   const int64_t slots = 148 * (row_tile(rows) == 4 ? 4 : 3), hist = histories(c, rows, false);
   const int steps = (c.cap + kStep - 1) / kStep;
   int size = 1;
   while (size < 16 && hist * size * 2 <= (size == 8 ? 148 : slots) && steps > kWarps * size) size *= 2;
-  return steps <= 8 * kWarps * size ? size : 0;
+  return steps <= (hist * size <= 148 ? 12 : 8) * kWarps * size ? size : 0;
 }
 
-// Where a cluster of 16 has more than a step for each warp, its CTAs, which have
-// an SM each, get twice the warps.
-bool token_cluster_is_wide(const Cache& c, int cluster) {
-  return cluster == 16 && (c.cap + kStep - 1) / kStep > kWarps * 16;
+// Where there is an SM for each CTA and more than a step for each of its warps,
+// the CTAs have twice the warps (4096 tokens of 4 heads 8.8 -> 8.1 us; 10007
+// tokens of 4 heads, rows of five tokens, 12.1 -> 9.7).
+bool token_cluster_is_wide(const Cache& c, int rows, int cluster) {
+  return histories(c, rows, false) * cluster <= 148 && (c.cap + kStep - 1) / kStep > kWarps * cluster;
 }
 
 // Rows of pieces: (slots) x (rows of a tile); none for clusters.
@@ -790,7 +794,7 @@ static cudaError_t token_fwd_d(const FwdParams4& p, cudaStream_t s) {
   const int rows = p.heads_q / p.c.heads * p.sq;
   const int cluster = token_cluster(p.c, rows);
   if (cluster > 0)
-    return token_cluster_is_wide(p.c, cluster) ? token_fwd_cluster<D, NT, 2 * kWarps>(p, cluster, s)
+    return token_cluster_is_wide(p.c, rows, cluster) ? token_fwd_cluster<D, NT, 2 * kWarps>(p, cluster, s)
                                                : token_fwd_cluster<D, NT, kWarps>(p, cluster, s);
   using R = Ring<D, NT, kWarps>;
   static SmemRecord have;
