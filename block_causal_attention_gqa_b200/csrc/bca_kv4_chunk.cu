@@ -21,7 +21,8 @@
 // read the same keys at the same time), and the units that are left over cut
 // into equal parts; kv4_chunk_combine_kernel joins their pieces.  In whole units
 // alone 540 of them take 4 rounds of 148 where 3.65 would do (1508 us against
-// XX), and 64 leave most SMs idle.  The barriers' phases run on from unit to
+// 1467 to 1500: there the power limit sets the clock), and 64 leave most SMs
+// idle.  The barriers' phases run on from unit to
 // unit, so the next unit's copies and first product overlap the last one's end.
 //
 // Weights (kv4_chunk_weights_kernel).  w_j sums over queries, so the tile is

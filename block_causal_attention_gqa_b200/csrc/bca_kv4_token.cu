@@ -31,15 +31,17 @@
 //   - P is scaled by 2^7 (reference m - 7) and m moves only when a score passes
 //     it by 8, so P stays below 2^15 in fp16 and loses nothing above 2^-31.
 //   - Each warp streams its own steps of 32 tokens through its own ring of
-//     bulk copies (one lane issues, mbarriers complete), so
-//     warps do not wait for one another until the end.
+//     bulk copies (one lane issues, mbarriers complete), so warps do not wait for
+//     one another until the end.  (Four small CTAs an SM; one of 16 warps, with
+//     or without a barrier every few steps to keep them together, took 80 to 84
+//     us where these take 77.)
 //
 // Split.  The steps of all histories (batch element, head, row tile) are laid
 // end to end and cut into equal parts, one for each CTA of the grid, so
 // histories of any number and lengths keep every SM busy to the end.  A part of
 // one history is a piece; piece (CTA c, history h) has slot c + h of the
-// workspace, which no other has.  kv4_combine_kernel joins the pieces' (m, l,
-// O).
+// workspace, which no other has.  kv4_token_combine_kernel joins the pieces'
+// (m, l, O).
 //
 // Short histories (token_cluster() says which) are a matter of latency: there a
 // cluster of up to 16 CTAs takes a history, joins its parts through

@@ -387,6 +387,9 @@ size_t magi_bca_kv4_weights_workspace_size(const magi_bca_kv4_cache* cache, cons
  * overlap out and lse.
  *   out bf16, lse fp32 [batch, heads_q, seqlen_q] (NULL: not wanted).  A row
  * with no key at all gets out = 0 and lse = -inf.
+ * Queries enter the products as fp16 numbers once they are normalised and
+ * multiplied by gamma_q, gamma_k and softmax_scale * log2(e): a feature beyond
+ * 65504 there is outside what is supported (so too in magi_bca_kv4_weights).
  * Repeated calls give the same bits. */
 int magi_bca_kv4_fwd(const magi_bca_bf16* q, const magi_bca_kv4_cache* cache, const int32_t* lengths,
                      const float* gamma_q, const float* gamma_k, const float* rope_q, const magi_bca_bf16* base_out,
