@@ -569,3 +569,53 @@ def test_calls_from_several_threads():
     for t in threads:
         t.join()
     assert not wrong
+
+
+# the forms of the kernel for few rows: clusters whose CTAs have an SM each and
+# twice the warps (of 16 CTAs, of 8), clusters of small CTAs, histories laid end to end
+FORMS = [(1, 1, 4, 1, 128, 24576, [24001]), (1, 1, 8, 8, 64, 2176, [2049]), (2, 2, 6, 2, 128, 4224, [4200, 2]),
+         (2, 5, 6, 2, 64, 10112, [0, 10007]), (1, 9, 3, 1, 128, 12288, [12287]), (2, 1, 16, 8, 64, 2176, [2100, 1]),
+         (3, 2, 12, 4, 128, 1152, [1100, 0, 64]), (1, 3, 10, 10, 128, 12288, [12200]), (18, 1, 4, 1, 64, 1280, [70 * i for i in range(18)]),
+         (4, 1, 8, 8, 128, 8192, [8192, 31, 0, 5000]), (1, 2, 40, 20, 64, 4096, [4000]),
+         (2, 1, 6, 3, 128, 32896, [32800, 5]), (1, 1, 16, 16, 64, 20480, [20333]), (1, 5, 8, 4, 128, 32768, [32111])]
+
+
+@pytest.mark.parametrize("base", [False, True])
+@pytest.mark.parametrize("case", FORMS)
+def test_attention_forms(case, base):
+    test_attention(True, case, base)
+
+
+@pytest.mark.parametrize("case", FORMS[:8])
+def test_attention_forms_repeat_the_same_bits(case):
+    B, Sq, Hq, H, D, cap, lengths = case
+    g = gen(cap + Hq)
+    cache = filled(g, B, H, D, cap, lengths)
+    q = randn(g, B, Sq, Hq, D).bfloat16()
+    gq, gk = gains(g, D)
+    n = ints(*lengths)
+    first = bca.magi_bca_kv4_fwd(q, cache, n, gq, gk)
+    for _ in range(20):
+        out, lse = bca.magi_bca_kv4_fwd(q, cache, n, gq, gk)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("kind", ["one value", "two values", "denormal", "steps", "negative"])
+def test_evict_weights_of_few_values(kind):
+    """Thresholds in a full bin, in the lowest and in the highest bits."""
+    g = gen(41)
+    B, H, D, cap, n, keep, recent = 1, 3, 64, 4352, 4300, 2000, 9
+    cache = filled(g, B, H, D, cap, [cap], behind=False)
+    r = torch.rand(B, H, cap, generator=g, device=DEV)
+    w = {"one value": torch.full_like(r, 0.25), "two values": (r < 0.3).float() * 2 - 1,
+         "denormal": (r * 1000).round() * 2.0 ** -149, "steps": 1 + (r * 300).round() * 2.0 ** -23,
+         "negative": -torch.exp(20 * r - 10)}[kind].contiguous()
+    to, to_w = bca.magi_bca_kv4_cache(B, H, D, 2048), torch.zeros(B, H, 2048, device=DEV)
+    left, index = bca.magi_bca_kv4_evict(cache, w, ints(n), keep, recent, to, to_w)
+    assert left.item() == keep
+    cand = w[0, :, :n - recent].double().cpu()
+    order = torch.sort(-cand, dim=-1, stable=True)[1][:, :keep - recent].sort(-1)[0]
+    want = torch.cat((order, torch.arange(n - recent, n).expand(H, recent)), -1)
+    assert torch.equal(index[0].cpu().long(), want)
+    assert torch.equal(to_w[0, :, :keep].cpu(), torch.gather(w[0].cpu(), 1, want))
+    assert bca.magi_bca_last_device_status() == 0
